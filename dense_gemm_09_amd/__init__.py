@@ -27,6 +27,9 @@ STATUS = ["GEMM_OK", "GEMM_ERR_NULL_POINTER", "GEMM_ERR_BAD_DIM", "GEMM_ERR_BAD_
           "GEMM_ERR_BAD_ENUM", "GEMM_ERR_UNSUPPORTED", "GEMM_ERR_WORKSPACE_TOO_SMALL",
           "GEMM_ERR_HIP"]
 EXPORTS = ["gemm_bf16", "gemm_bf16_noalloc", "gemm_fp8_scaled", "gemm_mxfp8", "gemm_bf16_quant", "gemm_fp8_scaled_quant",
+           "gemm_int8_scaled", "gemm_int8_scaled_quant", "gemm_quantize_int8_rows",
+           "gemm_int8_col_sums", "gemm_grouped_bf16", "gemm_grouped_fp8_scaled",
+           "gemm_grouped_int8_scaled", "gemm_grouped_bf16_wgrad",
            "gemm_quantize_fp8_rows", "gemm_pack_b", "gemm_workspace_size", "gemm_plan",
            "gemm_status_string"]
 
@@ -76,6 +79,31 @@ def lib() -> ctypes.CDLL:
         L.gemm_fp8_scaled_quant.argtypes = [_I64, _I64, _I64, _F32, _P, _I64, _I32, _P, _I64,
                                             _I32, _P, _P, _P, _I32, _P, _P, _P, _I64, _I32, _P,
                                             _SZ, _P]
+        L.gemm_int8_scaled.restype = _I32
+        L.gemm_int8_scaled.argtypes = [_I64, _I64, _I64, _F32, _P, _I64, _I32, _P, _I64, _I32, _P,
+                                       _P, _P, _P, _F32, _P, _I64, _I32, _P, _I32, _P, _SZ, _P]
+        L.gemm_int8_scaled_quant.restype = _I32
+        L.gemm_int8_scaled_quant.argtypes = [_I64, _I64, _I64, _F32, _P, _I64, _I32, _P, _I64,
+                                             _I32, _P, _P, _P, _P, _P, _I32, _P, _P, _P, _I64,
+                                             _I32, _P, _SZ, _P]
+        L.gemm_quantize_int8_rows.restype = _I32
+        L.gemm_quantize_int8_rows.argtypes = [_I64, _I64, _P, _I64, _P, _I64, _P, _P]
+        L.gemm_int8_col_sums.restype = _I32
+        L.gemm_int8_col_sums.argtypes = [_I64, _I64, _P, _I64, _P, _P]
+        L.gemm_grouped_bf16.restype = _I32
+        L.gemm_grouped_bf16.argtypes = [_I64, _I64, _I64, _I64, _F32, _P, _I64, _P, _P, _I64, _I32,
+                                        _I64, _F32, _P, _I64, _I32, _P, _I32, _P]
+        L.gemm_grouped_fp8_scaled.restype = _I32
+        L.gemm_grouped_fp8_scaled.argtypes = [_I64, _I64, _I64, _I64, _F32, _P, _I64, _P, _P, _I64,
+                                              _I32, _I64, _P, _P, _F32, _P, _I64, _I32, _P, _I32,
+                                              _P]
+        L.gemm_grouped_int8_scaled.restype = _I32
+        L.gemm_grouped_int8_scaled.argtypes = [_I64, _I64, _I64, _I64, _F32, _P, _I64, _P, _P,
+                                               _I64, _I32, _I64, _P, _P, _P, _P, _F32, _P, _I64,
+                                               _I32, _P, _I32, _P]
+        L.gemm_grouped_bf16_wgrad.restype = _I32
+        L.gemm_grouped_bf16_wgrad.argtypes = [_I64, _I64, _I64, _I64, _F32, _P, _I64, _P, _I64, _P,
+                                              _F32, _P, _I64, _I64, _I32, _P]
         L.gemm_pack_b.restype = _I32
         L.gemm_pack_b.argtypes = [_I64, _I64, _P, _I64, _I32, _I32, _P, _I64, _P]
         L.gemm_quantize_fp8_rows.restype = _I32
@@ -258,6 +286,131 @@ def gemm_fp8_scaled_quant(M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, sc
         raise GemmError(st, "gemm_fp8_scaled_quant")
 
 
+def _check_int8(M, N, scale_a, zero_a, scale_b, sum_b):
+    if M > 0 and N > 0:
+        _need(scale_a, 4 * M, "scale_a")
+        _need(zero_a, 4 * M, "zero_a")
+        _need(scale_b, 4 * N, "scale_b")
+        _need(sum_b, 4 * N, "sum_b")
+
+
+def gemm_int8_scaled(M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, scale_a, zero_a, scale_b,
+                     sum_b, beta, C, ldc, c_dtype, bias=None, act=ACT_NONE, workspace=None,
+                     workspace_bytes=None, stream=None):
+    """C = act(alpha * scale_a[m] scale_b[n] * (A - zero_a[m]) B + beta * C + bias), INT8 inputs.
+
+    zero_a (INT32[M]) and sum_b (INT32[N], int8_col_sums of B): both None for symmetric codes.
+    """
+    L = lib()
+    _check_operands(M, N, K, A, lda, layout_a, B, ldb, layout_b, C, ldc, c_dtype, 1, bias)
+    _check_int8(M, N, scale_a, zero_a, scale_b, sum_b)
+    workspace, workspace_bytes = _workspace(M, N, K, True, workspace, workspace_bytes, stream)
+    st = L.gemm_int8_scaled(M, N, K, alpha, _ptr(A), lda, layout_a, _ptr(B), ldb, layout_b,
+                            _ptr(scale_a), _ptr(zero_a), _ptr(scale_b), _ptr(sum_b), beta,
+                            _ptr(C), ldc, c_dtype, _ptr(bias), act, _ptr(workspace),
+                            workspace_bytes, _stream(stream))
+    if st != 0:
+        raise GemmError(st, "gemm_int8_scaled")
+
+
+def gemm_int8_scaled_quant(M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, scale_a, zero_a,
+                           scale_b, sum_b, bias, act, out_scale, out_zero, Q, ldq, q_dtype,
+                           workspace=None, workspace_bytes=None, stream=None):
+    """Q = quant(act(alpha * scale_a[m] scale_b[n] * (A - zero_a[m]) B + bias)) per row, INT8 inputs."""
+    L = lib()
+    _check_operands(M, N, K, A, lda, layout_a, B, ldb, layout_b, None, ldq, OUT_BF16, 1, bias)
+    _check_quant_out(M, N, Q, ldq, out_scale, out_zero)
+    _check_int8(M, N, scale_a, zero_a, scale_b, sum_b)
+    workspace, workspace_bytes = _workspace(M, N, K, True, workspace, workspace_bytes, stream)
+    st = L.gemm_int8_scaled_quant(M, N, K, alpha, _ptr(A), lda, layout_a, _ptr(B), ldb, layout_b,
+                                  _ptr(scale_a), _ptr(zero_a), _ptr(scale_b), _ptr(sum_b),
+                                  _ptr(bias), act, _ptr(out_scale), _ptr(out_zero), _ptr(Q), ldq,
+                                  q_dtype, _ptr(workspace), workspace_bytes, _stream(stream))
+    if st != 0:
+        raise GemmError(st, "gemm_int8_scaled_quant")
+
+
+def int8_col_sums(K, N, B, ldb, sums, stream=None):
+    """sums[n] = sum_k b(k, n) of an INT8 weight in COL layout (N rows of ldb), INT32."""
+    L = lib()
+    if N > 0:
+        _need(B, _extent(N, K, ldb), "B")
+        _need(sums, 4 * N, "sums")
+    st = L.gemm_int8_col_sums(K, N, _ptr(B), ldb, _ptr(sums), _stream(stream))
+    if st != 0:
+        raise GemmError(st, "gemm_int8_col_sums")
+
+
+def _check_grouped(G, T, N, K, A, lda, offsets, B, ldb, lb, stride_b, C, ldc, c_dtype, esize, bias):
+    if G > 0 and T > 0 and N > 0:
+        if K > 0:
+            _need(A, esize * _extent(T, K, lda), "A")
+            one = _extent(K, N, ldb) if lb == ROW else _extent(N, K, ldb)
+            _need(B, esize * ((G - 1) * stride_b + one), "B")
+        _need(offsets, 4 * (G + 1), "offsets")
+        _need(C, (4 if c_dtype == OUT_F32 else 2) * _extent(T, N, ldc), "C")
+        _need(bias, 2 * G * N, "bias")
+
+
+def gemm_grouped_bf16(G, T, N, K, alpha, A, lda, offsets, B, ldb, layout_b, stride_b, beta, C, ldc,
+                      c_dtype, bias=None, act=ACT_NONE, stream=None):
+    """C rows offsets[g]..offsets[g+1]-1 = act(alpha * A rows B_g + beta * C rows + bias[g]), BF16.
+
+    offsets: device INT32[G+1]; B_g at B + g * stride_b elements; bias [G, N].
+    """
+    L = lib()
+    _check_grouped(G, T, N, K, A, lda, offsets, B, ldb, layout_b, stride_b, C, ldc, c_dtype, 2, bias)
+    st = L.gemm_grouped_bf16(G, T, N, K, alpha, _ptr(A), lda, _ptr(offsets), _ptr(B), ldb,
+                             layout_b, stride_b, beta, _ptr(C), ldc, c_dtype, _ptr(bias), act,
+                             _stream(stream))
+    if st != 0:
+        raise GemmError(st, "gemm_grouped_bf16")
+
+
+def gemm_grouped_fp8_scaled(G, T, N, K, alpha, A, lda, offsets, B, ldb, layout_b, stride_b, scale_a,
+                            scale_b, beta, C, ldc, c_dtype, bias=None, act=ACT_NONE, stream=None):
+    """gemm_grouped_bf16 for E4M3 operands: scale_a[T] per row, scale_b[G, N] per channel."""
+    L = lib()
+    _check_grouped(G, T, N, K, A, lda, offsets, B, ldb, layout_b, stride_b, C, ldc, c_dtype, 1, bias)
+    _check_int8(T, G * N, scale_a, None, scale_b, None)
+    st = L.gemm_grouped_fp8_scaled(G, T, N, K, alpha, _ptr(A), lda, _ptr(offsets), _ptr(B), ldb,
+                                   layout_b, stride_b, _ptr(scale_a), _ptr(scale_b), beta, _ptr(C),
+                                   ldc, c_dtype, _ptr(bias), act, _stream(stream))
+    if st != 0:
+        raise GemmError(st, "gemm_grouped_fp8_scaled")
+
+
+def gemm_grouped_int8_scaled(G, T, N, K, alpha, A, lda, offsets, B, ldb, layout_b, stride_b,
+                             scale_a, zero_a, scale_b, sum_b, beta, C, ldc, c_dtype, bias=None,
+                             act=ACT_NONE, stream=None):
+    """gemm_grouped_bf16 for INT8 operands: scale_a, zero_a [T]; scale_b, sum_b [G, N]."""
+    L = lib()
+    _check_grouped(G, T, N, K, A, lda, offsets, B, ldb, layout_b, stride_b, C, ldc, c_dtype, 1, bias)
+    _check_int8(T, G * N, scale_a, zero_a, scale_b, sum_b)
+    st = L.gemm_grouped_int8_scaled(G, T, N, K, alpha, _ptr(A), lda, _ptr(offsets), _ptr(B), ldb,
+                                    layout_b, stride_b, _ptr(scale_a), _ptr(zero_a), _ptr(scale_b),
+                                    _ptr(sum_b), beta, _ptr(C), ldc, c_dtype, _ptr(bias), act,
+                                    _stream(stream))
+    if st != 0:
+        raise GemmError(st, "gemm_grouped_int8_scaled")
+
+
+def gemm_grouped_bf16_wgrad(G, T, N, K, alpha, D, ldd, X, ldx, offsets, beta, C, ldc, stride_c,
+                            c_dtype, stream=None):
+    """C_g[n, k] = alpha * sum of D[r, n] X[r, k] over group g's rows r + beta * C_g[n, k]."""
+    L = lib()
+    if G > 0 and N > 0 and K > 0:
+        if T > 0:
+            _need(D, 2 * _extent(T, N, ldd), "D")
+            _need(X, 2 * _extent(T, K, ldx), "X")
+        _need(offsets, 4 * (G + 1), "offsets")
+        _need(C, (4 if c_dtype == OUT_F32 else 2) * ((G - 1) * stride_c + _extent(N, K, ldc)), "C")
+    st = L.gemm_grouped_bf16_wgrad(G, T, N, K, alpha, _ptr(D), ldd, _ptr(X), ldx, _ptr(offsets),
+                                   beta, _ptr(C), ldc, stride_c, c_dtype, _stream(stream))
+    if st != 0:
+        raise GemmError(st, "gemm_grouped_bf16_wgrad")
+
+
 def pack_b(K, N, B, ldb, layout_b, elem_bytes, Bp, ldbp, stream=None):
     """One-time reorder of B (K x N) into K-major rows: Bp[n*ldbp + k] = b(k, n)."""
     L = lib()
@@ -280,6 +433,19 @@ def quantize_fp8_rows(M, K, X, ldx, Q, ldq, scale, stream=None):
     st = L.gemm_quantize_fp8_rows(M, K, _ptr(X), ldx, _ptr(Q), ldq, _ptr(scale), _stream(stream))
     if st != 0:
         raise GemmError(st, "gemm_quantize_fp8_rows")
+
+
+def quantize_int8_rows(M, K, X, ldx, Q, ldq, scale, stream=None):
+    """Per-token INT8 quantisation of BF16 rows: scale[m] = amax/127, Q = rne(x / scale)."""
+    L = lib()
+    if M > 0 and K > 0:
+        _need(X, 2 * _extent(M, K, ldx), "X")
+        _need(Q, _extent(M, K, ldq), "Q")
+    if M > 0:
+        _need(scale, 4 * M, "scale")
+    st = L.gemm_quantize_int8_rows(M, K, _ptr(X), ldx, _ptr(Q), ldq, _ptr(scale), _stream(stream))
+    if st != 0:
+        raise GemmError(st, "gemm_quantize_int8_rows")
 
 
 def _torch_stream(stream):

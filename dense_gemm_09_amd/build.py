@@ -16,13 +16,22 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgemm355.so")
 # (source, object name, extra defines). gemm_tile.hip is compiled once per
-# (ragged flag, output part) and once for the split-K reduction, so that its
-# kernel variants build in parallel.
-SOURCES = [("api.cpp", "api", []), ("gemm_skinny.hip", "gemm_skinny", []),
+# (ragged flag, output part) for the dense, the INT8 and the grouped products,
+# and once for the split-K reduction, so that its kernel variants build in
+# parallel.
+SOURCES = [("api.cpp", "api", []), ("grouped.cpp", "grouped", []), ("gemm_skinny.hip", "gemm_skinny", []),
            ("quant.hip", "quant", []), ("pack.hip", "pack", []),
            ("gemm_tile.hip", "gemm_reduce", ["-DG355_REDUCE=1"])]
 SOURCES += [("gemm_tile.hip", f"gemm_tile_r{r}_p{p}", [f"-DG355_RAGGED={r}", f"-DG355_PART={p}"])
             for r in (0, 1) for p in range(5)]
+SOURCES += [("gemm_tile.hip", f"gemm_i8_r{r}_p{p}",
+             ["-DG355_I8=1", f"-DG355_RAGGED={r}", f"-DG355_PART={p}"])
+            for r in (0, 1) for p in range(5)]
+SOURCES += [("gemm_tile.hip", f"gemm_grouped_r{r}_p{p}",
+             ["-DG355_GROUPED=1", f"-DG355_RAGGED={r}", f"-DG355_PART={p}"])
+            for r in (0, 1) for p in (1, 2)]
+SOURCES += [("gemm_tile.hip", f"gemm_wgrad_p{p}",
+             ["-DG355_WGRAD=1", "-DG355_RAGGED=0", f"-DG355_PART={p}"]) for p in (1, 2)]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

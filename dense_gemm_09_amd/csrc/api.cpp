@@ -158,11 +158,15 @@ hipError_t launch_tile(const Plan& plan, const LaunchSpec& spec, const GemmArgs&
        launch_tile_r0_p4},
       {launch_tile_r1_p0, launch_tile_r1_p1, launch_tile_r1_p2, launch_tile_r1_p3,
        launch_tile_r1_p4}};
+  static constexpr Fn kPartsI8[2][kOutParts] = {
+      {launch_i8_r0_p0, launch_i8_r0_p1, launch_i8_r0_p2, launch_i8_r0_p3, launch_i8_r0_p4},
+      {launch_i8_r1_p0, launch_i8_r1_p1, launch_i8_r1_p2, launch_i8_r1_p3, launch_i8_r1_p4}};
   const int part = plan.split > 1        ? PART_SPLIT
                    : spec.out == OUT_F32  ? PART_F32
                    : spec.out == OUT_BF16 ? PART_BF16
                    : spec.out == OUT_I8   ? PART_I8
                                           : PART_E4M3;
+  if (spec.i8) return kPartsI8[spec.ragged ? 1 : 0][part](plan, spec, args, stream);
   return kParts[spec.ragged ? 1 : 0][part](plan, spec, args, stream);
 }
 
@@ -186,15 +190,24 @@ struct MxScales {
   int64_t ldb;
 };
 
-// out_kind: OutKind. The quantised kinds (INT8, E4M3) come with beta == 0,
+// Zero points of A's rows and column sums of B (INT8 calls); both or neither.
+struct ZeroPoints {
+  const int32_t* zero_a;
+  const int32_t* sum_b;
+};
+
+// type: ElemType of A and B. out_kind: OutKind. The quantised kinds (INT8, E4M3) come with beta == 0,
 // the per-row output scale qscale and, for INT8 only, an optional zero point.
-// mx: block scales of an MX call (fp8 true, scale_a / scale_b unused), or null.
-gemm_status run(bool fp8, int64_t M, int64_t N, int64_t K, float alpha, const void* A,
+// mx: block scales of an MX call (type FP8, scale_a / scale_b unused), or null.
+// zero: INT8 calls only.
+gemm_status run(ElemType type, int64_t M, int64_t N, int64_t K, float alpha, const void* A,
                 int64_t lda, int layout_a, const void* B, int64_t ldb, int layout_b,
                 const float* scale_a, const float* scale_b, float beta, void* C, int64_t ldc,
                 int out_kind, const float* qscale, const int32_t* qzero, const void* bias,
                 int act, void* workspace, size_t workspace_bytes, void* stream,
-                const MxScales* mx = nullptr) {
+                const MxScales* mx = nullptr, const ZeroPoints* zero = nullptr) {
+  const bool fp8 = type == TY_FP8, i8 = type == TY_I8;
+  const bool bytes1 = fp8 || i8;  // one byte per element
   // ---- enums and sizes
   if (!valid_layout(layout_a) || !valid_layout(layout_b) || !valid_act(act))
     return GEMM_ERR_BAD_ENUM;
@@ -202,8 +215,9 @@ gemm_status run(bool fp8, int64_t M, int64_t N, int64_t K, float alpha, const vo
   if (out_kind == OUT_E4M3 && qzero != nullptr) return GEMM_ERR_UNSUPPORTED;
   if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
     return GEMM_ERR_BAD_DIM;
-  if (fp8 && (layout_a != GEMM_ROW_MAJOR || layout_b != GEMM_COL_MAJOR))
+  if (bytes1 && (layout_a != GEMM_ROW_MAJOR || layout_b != GEMM_COL_MAJOR))
     return GEMM_ERR_UNSUPPORTED;
+  if (i8 && K > kMaxInt8K) return GEMM_ERR_UNSUPPORTED;
   // ---- leading dimensions
   const int64_t need_lda = layout_a == GEMM_ROW_MAJOR ? K : M;
   const int64_t need_ldb = layout_b == GEMM_ROW_MAJOR ? N : K;
@@ -224,7 +238,8 @@ gemm_status run(bool fp8, int64_t M, int64_t N, int64_t K, float alpha, const vo
   // ---- pointers
   if (C == nullptr) return GEMM_ERR_NULL_POINTER;
   if (K > 0 && (A == nullptr || B == nullptr)) return GEMM_ERR_NULL_POINTER;
-  if (fp8 && !mx && (scale_a == nullptr || scale_b == nullptr)) return GEMM_ERR_NULL_POINTER;
+  if (bytes1 && !mx && (scale_a == nullptr || scale_b == nullptr)) return GEMM_ERR_NULL_POINTER;
+  if (i8 && (zero->zero_a == nullptr) != (zero->sum_b == nullptr)) return GEMM_ERR_NULL_POINTER;
   if (mx && K > 0) {
     if (mx->a == nullptr || mx->b == nullptr) return GEMM_ERR_NULL_POINTER;
     if ((reinterpret_cast<uintptr_t>(mx->a) & 3u) || (reinterpret_cast<uintptr_t>(mx->b) & 3u))
@@ -232,7 +247,7 @@ gemm_status run(bool fp8, int64_t M, int64_t N, int64_t K, float alpha, const vo
   }
   if (quant_out && qscale == nullptr) return GEMM_ERR_NULL_POINTER;
 
-  const Plan plan = make_plan(M, N, K, fp8);
+  const Plan plan = make_plan(M, N, K, bytes1);
   // Every tile size in use is >= 128, so this bounds the grid of any variant.
   if (((M + 127) / 128) * ((N + 127) / 128) * plan.split > INT32_MAX) return GEMM_ERR_BAD_DIM;
   if (plan.workspace > 0) {
@@ -241,10 +256,11 @@ gemm_status run(bool fp8, int64_t M, int64_t N, int64_t K, float alpha, const vo
   }
 
   // ---- how each operand reaches LDS
-  const int ce = fp8 ? 16 : 8;  // elements per 16-byte chunk
+  const int ce = bytes1 ? 16 : 8;  // elements per 16-byte chunk
   auto aligned16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
   LaunchSpec spec{};
   spec.fp8 = fp8;
+  spec.i8 = i8;
   spec.a_kmajor = layout_a == GEMM_ROW_MAJOR;
   spec.b_kmajor = layout_b == GEMM_COL_MAJOR;
   spec.out = out_kind;
@@ -256,20 +272,20 @@ gemm_status run(bool fp8, int64_t M, int64_t N, int64_t K, float alpha, const vo
   // chunk (the kernel writes each row's last, partial chunk itself), and rows
   // need not be 16-byte aligned: the buffer loads take any byte offset (BF16
   // elements must still be 2-byte aligned).
-  const int64_t es = fp8 ? 1 : 2;
+  const int64_t es = bytes1 ? 1 : 2;
   const auto under2g = [&](int64_t rows, int64_t ld) {
     return ((rows - 1) * ld + K) * es < (int64_t{1} << 31);
   };
   const auto rows16 = [&](const void* p, int64_t ld) { return aligned16(p) && ld % ce == 0; };
   const auto dma_ok = [&](bool kmajor, const void* p, int64_t ld, int64_t rows) {
     const bool even = (reinterpret_cast<uintptr_t>(p) & 1u) == 0;
-    return kmajor && under2g(rows, ld) && (fp8 || even);
+    return kmajor && under2g(rows, ld) && (bytes1 || even);
   };
   spec.loader_a = dma_ok(spec.a_kmajor, A, lda, M) ? LOAD_DIRECT : LOAD_GENERIC;
   spec.loader_b = dma_ok(spec.b_kmajor, B, ldb, N) ? LOAD_DIRECT : LOAD_GENERIC;
   // BF16 B stored N-contiguous: DMA into an N-major tile (transposing reads)
   // when its rows are 16-byte aligned, N is a multiple of 8 and A is DMA-fed.
-  if (!fp8 && !spec.b_kmajor && spec.loader_a == LOAD_DIRECT && ldb % 8 == 0 && N % 8 == 0 &&
+  if (!bytes1 && !spec.b_kmajor && spec.loader_a == LOAD_DIRECT && ldb % 8 == 0 && N % 8 == 0 &&
       aligned16(B) && ((K - 1) * ldb + N) * es < (int64_t{1} << 31))
     spec.loader_b = LOAD_DIRECT_N;
   if (K == 0) spec.loader_a = spec.loader_b = LOAD_DIRECT;  // nothing is loaded
@@ -279,15 +295,15 @@ gemm_status run(bool fp8, int64_t M, int64_t N, int64_t K, float alpha, const vo
   // MX runs on the DMA-fed tile kernel only (no skinny kernel).
   if (mx && !direct) return GEMM_ERR_UNSUPPORTED;
   // K ends inside a 16-byte chunk of a DMA-fed K-major row: the tile kernels
-  // that write that chunk themselves. (FP8 with one operand not DMA-fed reads
-  // both through registers.)
-  spec.ragged = !k_ok && (direct || (!fp8 && (spec.loader_a == LOAD_DIRECT ||
+  // that write that chunk themselves. (FP8 or INT8 with one operand not DMA-fed
+  // reads both through registers.)
+  spec.ragged = !k_ok && (direct || (!bytes1 && (spec.loader_a == LOAD_DIRECT ||
                                               spec.loader_b == LOAD_DIRECT)));
   // The skinny kernel reads K-major operands with 16-byte aligned rows and K a
   // multiple of the chunk only.
   const bool skinny_ok = direct && !mx && spec.loader_b == LOAD_DIRECT && k_ok &&
                          rows16(A, lda) && rows16(B, ldb);
-  Plan p = (plan.kernel == KERNEL_SKINNY && !skinny_ok) ? make_tile_plan(M, N, K, fp8) : plan;
+  Plan p = (plan.kernel == KERNEL_SKINNY && !skinny_ok) ? make_tile_plan(M, N, K, bytes1) : plan;
   if (p.kernel == KERNEL_TILE && !direct) {
     p.bm = 128;
     p.bn = 128;
@@ -303,6 +319,10 @@ gemm_status run(bool fp8, int64_t M, int64_t N, int64_t K, float alpha, const vo
   a.workspace = static_cast<float*>(workspace);
   a.qscale = quant_out ? qscale : nullptr;
   a.qzero = out_kind == OUT_I8 ? qzero : nullptr;
+  if (i8) {
+    a.zero_a = zero->zero_a;
+    a.sum_b = zero->sum_b;
+  }
   if (mx) {
     a.mx_a = static_cast<const uint8_t*>(mx->a);
     a.mx_b = static_cast<const uint8_t*>(mx->b);
@@ -384,7 +404,7 @@ gemm_status gemm_bf16(int64_t M, int64_t N, int64_t K, float alpha, const void* 
                       float beta, void* C, int64_t ldc, gemm_out_dtype c_dtype, const void* bias,
                       gemm_act act, void* workspace, size_t workspace_bytes, void* stream) {
   if (!valid_out(c_dtype)) return GEMM_ERR_BAD_ENUM;
-  return run(false, M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, nullptr, nullptr, beta,
+  return run(TY_BF16, M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, nullptr, nullptr, beta,
              C, ldc, c_dtype, nullptr, nullptr, bias, act, workspace, workspace_bytes, stream);
 }
 
@@ -406,7 +426,7 @@ gemm_status gemm_bf16_noalloc(int64_t M, int64_t N, int64_t K, float alpha, cons
     const gemm_status st = scratch_of_current_device(&ws);
     if (st != GEMM_OK) return st;
   }
-  return run(false, M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, nullptr, nullptr, beta,
+  return run(TY_BF16, M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, nullptr, nullptr, beta,
              C, ldc, c_dtype, nullptr, nullptr, bias, act, ws, ws ? kNoAllocScratchBytes : 0,
              stream);
 }
@@ -418,7 +438,7 @@ gemm_status gemm_fp8_scaled(int64_t M, int64_t N, int64_t K, float alpha, const 
                             const void* bias, gemm_act act, void* workspace,
                             size_t workspace_bytes, void* stream) {
   if (!valid_out(c_dtype)) return GEMM_ERR_BAD_ENUM;
-  return run(true, M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, scale_a, scale_b, beta,
+  return run(TY_FP8, M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, scale_a, scale_b, beta,
              C, ldc, c_dtype, nullptr, nullptr, bias, act, workspace, workspace_bytes, stream);
 }
 
@@ -429,7 +449,7 @@ gemm_status gemm_mxfp8(int64_t M, int64_t N, int64_t K, float alpha, const void*
                        gemm_act act, void* workspace, size_t workspace_bytes, void* stream) {
   if (!valid_out(c_dtype)) return GEMM_ERR_BAD_ENUM;
   const MxScales mx{scale_a, ldsa, scale_b, ldsb};
-  return run(true, M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, nullptr, nullptr, beta, C,
+  return run(TY_FP8, M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, nullptr, nullptr, beta, C,
              ldc, c_dtype, nullptr, nullptr, bias, act, workspace, workspace_bytes, stream, &mx);
 }
 
@@ -440,7 +460,7 @@ gemm_status gemm_bf16_quant(int64_t M, int64_t N, int64_t K, float alpha, const 
                             int64_t ldq, gemm_qout_dtype q_dtype, void* workspace,
                             size_t workspace_bytes, void* stream) {
   if (!valid_qout(q_dtype)) return GEMM_ERR_BAD_ENUM;
-  return run(false, M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, nullptr, nullptr, 0.f,
+  return run(TY_BF16, M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, nullptr, nullptr, 0.f,
              Q, ldq, qout_kind(q_dtype), out_scale, out_zero, bias, act, workspace,
              workspace_bytes, stream);
 }
@@ -453,9 +473,66 @@ gemm_status gemm_fp8_scaled_quant(int64_t M, int64_t N, int64_t K, float alpha, 
                                   int64_t ldq, gemm_qout_dtype q_dtype, void* workspace,
                                   size_t workspace_bytes, void* stream) {
   if (!valid_qout(q_dtype)) return GEMM_ERR_BAD_ENUM;
-  return run(true, M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, scale_a, scale_b, 0.f,
+  return run(TY_FP8, M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, scale_a, scale_b, 0.f,
              Q, ldq, qout_kind(q_dtype), out_scale, out_zero, bias, act, workspace,
              workspace_bytes, stream);
+}
+
+gemm_status gemm_int8_scaled(int64_t M, int64_t N, int64_t K, float alpha, const void* A,
+                             int64_t lda, gemm_layout layout_a, const void* B, int64_t ldb,
+                             gemm_layout layout_b, const float* scale_a, const int32_t* zero_a,
+                             const float* scale_b, const int32_t* sum_b, float beta, void* C,
+                             int64_t ldc, gemm_out_dtype c_dtype, const void* bias, gemm_act act,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  if (!valid_out(c_dtype)) return GEMM_ERR_BAD_ENUM;
+  const ZeroPoints zero{zero_a, sum_b};
+  return run(TY_I8, M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, scale_a, scale_b, beta, C,
+             ldc, c_dtype, nullptr, nullptr, bias, act, workspace, workspace_bytes, stream,
+             nullptr, &zero);
+}
+
+gemm_status gemm_int8_scaled_quant(int64_t M, int64_t N, int64_t K, float alpha, const void* A,
+                                   int64_t lda, gemm_layout layout_a, const void* B, int64_t ldb,
+                                   gemm_layout layout_b, const float* scale_a,
+                                   const int32_t* zero_a, const float* scale_b,
+                                   const int32_t* sum_b, const void* bias, gemm_act act,
+                                   const float* out_scale, const int32_t* out_zero, void* Q,
+                                   int64_t ldq, gemm_qout_dtype q_dtype, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  if (!valid_qout(q_dtype)) return GEMM_ERR_BAD_ENUM;
+  const ZeroPoints zero{zero_a, sum_b};
+  return run(TY_I8, M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, scale_a, scale_b, 0.f, Q,
+             ldq, qout_kind(q_dtype), out_scale, out_zero, bias, act, workspace, workspace_bytes,
+             stream, nullptr, &zero);
+}
+
+gemm_status gemm_quantize_int8_rows(int64_t M, int64_t K, const void* X, int64_t ldx, void* Q,
+                                    int64_t ldq, float* scale, void* stream) {
+  if (M < 0 || K < 0 || M > kMaxDim || K > kMaxDim) return GEMM_ERR_BAD_DIM;
+  if (ldx < std::max<int64_t>(1, K) || ldq < std::max<int64_t>(1, K)) return GEMM_ERR_BAD_LD;
+  if (M == 0) return GEMM_OK;
+  if (scale == nullptr) return GEMM_ERR_NULL_POINTER;
+  if (K > 0 && (X == nullptr || Q == nullptr)) return GEMM_ERR_NULL_POINTER;
+  const auto aligned = [](const void* p, uintptr_t a) {
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+  };
+  const bool vec = K % 8 == 0 && ldx % 8 == 0 && ldq % 8 == 0 && aligned(X, 16) && aligned(Q, 8);
+  (void)hipGetLastError();
+  return launch_quantize_int8_rows(M, K, X, ldx, Q, ldq, scale, vec,
+                                   static_cast<hipStream_t>(stream)) == hipSuccess
+             ? GEMM_OK : GEMM_ERR_HIP;
+}
+
+gemm_status gemm_int8_col_sums(int64_t K, int64_t N, const void* B, int64_t ldb, int32_t* sums,
+                               void* stream) {
+  if (K < 0 || N < 0 || K > kMaxDim || N > kMaxDim) return GEMM_ERR_BAD_DIM;
+  if (K > kMaxInt8K) return GEMM_ERR_UNSUPPORTED;
+  if (ldb < std::max<int64_t>(1, K)) return GEMM_ERR_BAD_LD;
+  if (N == 0) return GEMM_OK;
+  if (sums == nullptr || (K > 0 && B == nullptr)) return GEMM_ERR_NULL_POINTER;
+  (void)hipGetLastError();
+  return launch_int8_row_sums(N, K, B, ldb, sums, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? GEMM_OK : GEMM_ERR_HIP;
 }
 
 gemm_status gemm_quantize_fp8_rows(int64_t M, int64_t K, const void* X, int64_t ldx, void* Q,

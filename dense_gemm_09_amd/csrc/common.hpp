@@ -8,6 +8,7 @@ namespace g355 {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -16,6 +17,9 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 #define G355_LDS __attribute__((address_space(3)))
 
 enum Act : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU_ERF = 2, ACT_GELU_TANH = 3 };
+
+// Operand element types.
+enum ElemType : int { TY_BF16 = 0, TY_FP8 = 1, TY_I8 = 2 };
 
 // What the epilogue writes: FP32 or BF16 C (read back when beta != 0), or a
 // quantised tensor of one byte per element with a per-row output scale
@@ -28,8 +32,8 @@ struct GemmArgs {
   const void* B;
   void* C;
   const uint16_t* bias;   // BF16[N] or nullptr
-  const float* scale_a;   // FP32[M] (FP8 only)
-  const float* scale_b;   // FP32[N] (FP8 only)
+  const float* scale_a;   // FP32[M] (FP8 and INT8 only)
+  const float* scale_b;   // FP32[N] (FP8 and INT8 only)
   float* workspace;       // split-K partials
   const float* qscale;    // FP32[M] output scale (quantised outputs)
   const int32_t* qzero;   // INT32[M] output zero point (INT8 output) or nullptr
@@ -47,7 +51,19 @@ struct GemmArgs {
   int split_k;            // number of K partitions
   int k_split_len;        // elements of K per partition (multiple of the K tile)
   int tiles_m, tiles_n;
+  const int32_t* zero_a;  // INT32[M] zero points of A's rows (INT8 only) or nullptr
+  const int32_t* sum_b;   // INT32[N] column sums of B, with zero_a
+  // Products grouped by rows:
+  const int32_t* offsets; // INT32[groups + 1]: group g has rows offsets[g] .. offsets[g+1]-1
+  int groups;
+  int rows_total;         // rows of A and C (weight gradient: of A and B)
+  int64_t stride_b;       // elements from one group's B (weight gradient: C) to the next
 };
+
+// Tiles per group from which the weight gradient deals each group's tiles to
+// the XCDs in eighths (below, workgroups go round robin: an eighth of fewer
+// tiles than this shares little).
+constexpr int kWgradXcdTiles = 64;
 
 // ---------------------------------------------------------------- conversions
 
@@ -88,6 +104,17 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 __device__ __forceinline__ uint32_t quant_i8(float y, float s, float zp) {
   const float v = __builtin_amdgcn_fmed3f(fmaf(y, s, zp), -128.f, 127.f);
   return static_cast<uint32_t>(static_cast<int>(__builtin_rintf(v))) & 0xffu;
+}
+
+// The INT32 sum of an INT8 product as FP32, the zero point's share
+// za * sum_k b(k,n) taken off. Without one the sum is rounded to FP32 (2^-24
+// relative; exact below 2^24). With one, the two integers can nearly cancel,
+// so the difference is taken in double, which holds the sum, the product (za
+// below 2^24 in magnitude, |sum_b| below 2^28) and their difference exactly,
+// and only then rounded.
+__device__ __forceinline__ float i8_sum(int acc, bool has_zero, int za, double sum_b) {
+  if (!has_zero) return static_cast<float>(acc);
+  return static_cast<float>(static_cast<double>(acc) - static_cast<double>(za) * sum_b);
 }
 
 // Element `off` of an output of kind OUT. s and zp: the row's output scale and

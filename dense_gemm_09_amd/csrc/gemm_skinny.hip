@@ -14,7 +14,7 @@
 //   flight.
 // * A (M x K, a few hundred KB at most) is read from L2 by every workgroup.
 // * The inner product uses v_mfma_f32_16x16x32_bf16 / the 16x16x128 FP8
-//   (f8f6f4, E4M3, scale 2^0) MFMA with M padded to 16 (MB blocks of 16 rows;
+//   (f8f6f4, E4M3, scale 2^0) / v_mfma_i32_16x16x64_i8 MFMA with M padded to 16 (MB blocks of 16 rows;
 //   rows past M are zero lanes and are never stored). A and B fragments hold
 //   the same K indices in the same register slots.
 // * The KW partial sums are added through LDS in wave order 0..KW-1 (fixed
@@ -33,16 +33,39 @@ namespace g355 {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
-template <bool FP8, int MB, int KW, int U>
+template <int TY, int MB, int KW, int U>
 struct SkinnyCfg {
-  static constexpr int ES = FP8 ? 1 : 2;
-  static constexpr int KSTEP = FP8 ? 128 : 32;        // K elements per MFMA
-  static constexpr int LANE_BYTES = FP8 ? 32 : 16;    // bytes of one operand row per lane per MFMA
+  static constexpr int ES = TY == TY_BF16 ? 2 : 1;
+  static constexpr int KSTEP = TY == TY_FP8 ? 128 : TY == TY_I8 ? 64 : 32;  // K elements per MFMA
+  static constexpr int LANE_BYTES = TY == TY_FP8 ? 32 : 16;  // bytes of one operand row per lane per MFMA
   static constexpr int NT = KW * 64;
+  using Acc = std::conditional_t<TY == TY_I8, i32x4, f32x4>;
 };
 
+// One MFMA of type TY (operands padded to eight registers for every type).
+template <int TY, class Acc>
+__device__ __forceinline__ Acc skinny_mfma(const i32x8& a, const i32x8& b, const Acc& c) {
+  const i32x4 a4 = {a[0], a[1], a[2], a[3]}, b4 = {b[0], b[1], b[2], b[3]};
+  if constexpr (TY == TY_FP8)
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
+  else if constexpr (TY == TY_I8)
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a4, b4, c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a4),
+                                                   __builtin_bit_cast(bf16x8_t, b4), c, 0, 0, 0);
+}
+
+// An accumulated sum as FP32 (INT8: less the zero point's share).
+__device__ __forceinline__ float skinny_sum(const GemmArgs&, float v, int, int) { return v; }
+__device__ __forceinline__ float skinny_sum(const GemmArgs& p, int v, int m, int n) {
+  const bool has_zero = p.zero_a != nullptr;
+  return i8_sum(v, has_zero, has_zero ? p.zero_a[m] : 0,
+                has_zero ? static_cast<double>(p.sum_b[n]) : 0.0);
+}
+
 template <class S, int OUT, int MB, int ACT>
-__device__ __forceinline__ void skinny_epilogue(const GemmArgs& p, const f32x4 (&acc)[MB], int n0,
+__device__ __forceinline__ void skinny_epilogue(const GemmArgs& p,
+                                                const typename S::Acc (&acc)[MB], int n0,
                                                 int lane) {
   const int n = n0 + (lane & 15);
   if (n >= p.N) return;
@@ -55,7 +78,7 @@ __device__ __forceinline__ void skinny_epilogue(const GemmArgs& p, const f32x4 (
     for (int e = 0; e < 4; ++e) {
       const int m = 16 * mb + 4 * (lane >> 4) + e;
       if (m >= p.M) continue;
-      float z = acc[mb][e];
+      float z = skinny_sum(p, acc[mb][e], m, n);
       if constexpr (S::ES == 1) z = z * (p.scale_a[m] * sb);
       z = p.alpha * z;
       const int64_t off = static_cast<int64_t>(m) * p.ldc + n;
@@ -70,10 +93,11 @@ __device__ __forceinline__ void skinny_epilogue(const GemmArgs& p, const f32x4 (
   }
 }
 
-template <bool FP8, int MB, int KW, int U, int OUT>
+template <int TY, int MB, int KW, int U, int OUT>
 __global__ void __launch_bounds__(KW * 64) gemm_skinny_kernel(GemmArgs p) {
-  using S = SkinnyCfg<FP8, MB, KW, U>;
-  __shared__ __attribute__((aligned(16))) f32x4 red[KW][MB][64];
+  using S = SkinnyCfg<TY, MB, KW, U>;
+  using Acc = typename S::Acc;
+  __shared__ __attribute__((aligned(16))) Acc red[KW][MB][64];
 
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
@@ -100,9 +124,9 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_kernel(GemmArgs p) {
                static_cast<int64_t>(a_ok[mb] ? m : 0) * p.lda * S::ES;
   }
 
-  f32x4 acc[MB];
+  Acc acc[MB];
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) acc[mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int mb = 0; mb < MB; ++mb) acc[mb] = Acc{0, 0, 0, 0};
 
   // One MFMA's worth of a lane's operand: 16 (BF16) or 32 (FP8) bytes at
   // element k = k0 + g * (LANE_BYTES / ES); chunks at or past K are zero
@@ -136,15 +160,7 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_kernel(GemmArgs p) {
     for (int u = 0; u < U; ++u) {
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
-        if constexpr (FP8) {
-          acc[mb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av[u][mb], bv[u], acc[mb], 0,
-                                                                     0, 0, 127, 0, 127);
-        } else {
-          const i32x4 a4 = {av[u][mb][0], av[u][mb][1], av[u][mb][2], av[u][mb][3]};
-          const i32x4 b4 = {bv[u][0], bv[u][1], bv[u][2], bv[u][3]};
-          acc[mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8_t, a4), __builtin_bit_cast(bf16x8_t, b4), acc[mb], 0, 0, 0);
-        }
+        acc[mb] = skinny_mfma<TY>(av[u][mb], bv[u], acc[mb]);
       }
     }
   }
@@ -156,7 +172,7 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_kernel(GemmArgs p) {
   if (wave != 0) return;
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb) {
-    f32x4 s = red[0][mb][lane];
+    Acc s = red[0][mb][lane];
 #pragma unroll
     for (int w = 1; w < KW; ++w) s += red[w][mb][lane];
     acc[mb] = s;
@@ -185,14 +201,16 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_kernel(GemmArgs p) {
 // The last round is split for BF16 only: measured at K = 4096, it takes BF16
 // M = 1 / 16, N = 18432 from 30.1 / 35.0 to 28.9 / 33.2 us, and leaves FP8
 // (19 us, whose rate is not set by that round) where it was.
-template <bool FP8>
-constexpr bool kSplitLastRound = !FP8;
+template <int TY>
+constexpr bool kSplitLastRound = TY == TY_BF16;
 
-template <bool FP8, int KW, int KSM, int NBUF, int OUT, int ACT>
+template <int TY, int KW, int KSM, int NBUF, int OUT, int ACT>
 __global__ void __launch_bounds__(KW * 64) gemm_skinny_stream_kernel(GemmArgs p) {
-  using S = SkinnyCfg<FP8, 1, KW, 1>;
+  using S = SkinnyCfg<TY, 1, KW, 1>;
+  using Acc = typename S::Acc;
+  constexpr bool FP8 = TY == TY_FP8;
   using Frag = typename std::conditional<FP8, i32x8, i32x4>::type;
-  __shared__ __attribute__((aligned(16))) f32x4 red[2][KW][64];
+  __shared__ __attribute__((aligned(16))) Acc red[2][KW][64];
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -237,11 +255,11 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_stream_kernel(GemmArgs p)
   // Items 0..R-1 are the whole blocks blockIdx.x + i G; item R is its share
   // of the last, partial round (T blocks), whole or halved as described above.
   const int R = nblk / G, T = nblk - R * G;
-  const bool halves = kSplitLastRound<FP8> && T > 0 && 2 * T <= G;
+  const bool halves = kSplitLastRound<TY> && T > 0 && 2 * T <= G;
   const int bx = blockIdx.x;
   auto item = [&](int i, int& col0, int& width) -> bool {
     width = 16;
-    if constexpr (!kSplitLastRound<FP8>) {
+    if constexpr (!kSplitLastRound<TY>) {
       const int b = bx + i * G;
       col0 = 16 * b;
       return b < nblk;
@@ -268,7 +286,7 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_stream_kernel(GemmArgs p)
     int n = col0 + c;
     n = n < p.N ? n : p.N - 1;  // columns past N are computed but never stored
     const char* brow = static_cast<const char*>(p.B) + static_cast<int64_t>(n) * p.ldb * S::ES;
-    const bool in = !kSplitLastRound<FP8> || c < width;
+    const bool in = !kSplitLastRound<TY> || c < width;
 #pragma unroll
     for (int ks = 0; ks < KSM; ++ks) bv[ks] = ld(brow, kb + ks * S::KSTEP, in && ks < per);
   };
@@ -288,16 +306,16 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_stream_kernel(GemmArgs p)
       if (!item(i, col0, width)) return;
       int cn, wn;  // prefetch: NBUF - 1 items ahead
       if (item(i + NBUF - 1, cn, wn)) load_block(cn, wn, bv[(u + NBUF - 1) % NBUF]);
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      Acc acc = {0, 0, 0, 0};
 #pragma unroll
       for (int ks = 0; ks < KSM; ++ks) {
-        if constexpr (FP8)
-          acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av[ks], bv[u][ks], acc, 0, 0, 0,
-                                                                 127, 0, 127);
-        else
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, av[ks]),
-                                                        __builtin_bit_cast(bf16x8_t, bv[u][ks]),
-                                                        acc, 0, 0, 0);
+        if constexpr (FP8) {
+          acc = skinny_mfma<TY>(av[ks], bv[u][ks], acc);
+        } else {
+          const Frag a = av[ks], b = bv[u][ks];
+          acc = skinny_mfma<TY>(i32x8{a[0], a[1], a[2], a[3], 0, 0, 0, 0},
+                                i32x8{b[0], b[1], b[2], b[3], 0, 0, 0, 0}, acc);
+        }
       }
       red[i & 1][wave][lane] = acc;
       __syncthreads();
@@ -305,11 +323,12 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_stream_kernel(GemmArgs p)
       if (tid < 256) {
         const int r = tid >> 4, c = tid & 15;
         const int n = col0 + c;
-        if (r < p.M && (!kSplitLastRound<FP8> || c < width) && n < p.N) {
+        if (r < p.M && (!kSplitLastRound<TY> || c < width) && n < p.N) {
           const int src = 16 * (r >> 2) + c;
-          float z = red[i & 1][0][src][r & 3];
+          auto sum = red[i & 1][0][src][r & 3];
 #pragma unroll
-          for (int w = 1; w < KW; ++w) z += red[i & 1][w][src][r & 3];
+          for (int w = 1; w < KW; ++w) sum += red[i & 1][w][src][r & 3];
+          float z = skinny_sum(p, sum, r, n);
           if constexpr (S::ES == 1) z = z * (p.scale_a[r] * p.scale_b[n]);
           z = p.alpha * z;
           const int64_t off = static_cast<int64_t>(r) * p.ldc + n;
@@ -330,19 +349,19 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_stream_kernel(GemmArgs p)
 #ifndef G355_KERNELS_ONLY
 // KW = 16 K-split waves per workgroup; U k-steps of loads in flight per wave
 // (BF16 4 x 1 KB, FP8 2 x 2 KB). Chosen by a sweep at K = 4096, N = 4096..18432.
-template <bool FP8, int MB>
+template <int TY, int MB>
 static hipError_t launch_mb(const GemmArgs& a, int out, hipStream_t stream) {
   constexpr int KW = 16;
-  constexpr int U = FP8 ? 2 : 4;
+  constexpr int U = TY == TY_FP8 ? 2 : 4;
   const dim3 grid(static_cast<unsigned>((a.N + 15) / 16)), block(KW * 64);
   if (out == OUT_BF16)
-    hipLaunchKernelGGL((gemm_skinny_kernel<FP8, MB, KW, U, OUT_BF16>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((gemm_skinny_kernel<TY, MB, KW, U, OUT_BF16>), grid, block, 0, stream, a);
   else if (out == OUT_I8)
-    hipLaunchKernelGGL((gemm_skinny_kernel<FP8, MB, KW, U, OUT_I8>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((gemm_skinny_kernel<TY, MB, KW, U, OUT_I8>), grid, block, 0, stream, a);
   else if (out == OUT_E4M3)
-    hipLaunchKernelGGL((gemm_skinny_kernel<FP8, MB, KW, U, OUT_E4M3>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((gemm_skinny_kernel<TY, MB, KW, U, OUT_E4M3>), grid, block, 0, stream, a);
   else
-    hipLaunchKernelGGL((gemm_skinny_kernel<FP8, MB, KW, U, OUT_F32>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((gemm_skinny_kernel<TY, MB, KW, U, OUT_F32>), grid, block, 0, stream, a);
   return hipGetLastError();
 }
 
@@ -353,31 +372,31 @@ static hipError_t launch_mb(const GemmArgs& a, int out, hipStream_t stream) {
 // (M = 1 BF16 was already at ~5 TB/s: unchanged). Prefetching four FP8 blocks
 // ahead instead of two needs more than the 128 VGPRs a 16-wave workgroup may
 // use and spills (27 us).
-template <bool FP8, int OUT>
+template <int TY, int OUT>
 static hipError_t launch_stream_out(const GemmArgs& a, hipStream_t stream) {
-  constexpr int KW = 16, KSM = FP8 ? 2 : 8, NBUF = FP8 ? 3 : 2;
+  constexpr int KW = 16, KSM = TY == TY_FP8 ? 2 : TY == TY_I8 ? 4 : 8, NBUF = TY == TY_BF16 ? 2 : 3;
   const dim3 grid(static_cast<unsigned>(skinny_stream_grid(a.N))), block(KW * 64);
   if (a.act == ACT_NONE)
-    hipLaunchKernelGGL((gemm_skinny_stream_kernel<FP8, KW, KSM, NBUF, OUT, ACT_NONE>), grid, block,
+    hipLaunchKernelGGL((gemm_skinny_stream_kernel<TY, KW, KSM, NBUF, OUT, ACT_NONE>), grid, block,
                        0, stream, a);
   else if (a.act == ACT_RELU)
-    hipLaunchKernelGGL((gemm_skinny_stream_kernel<FP8, KW, KSM, NBUF, OUT, ACT_RELU>), grid, block,
+    hipLaunchKernelGGL((gemm_skinny_stream_kernel<TY, KW, KSM, NBUF, OUT, ACT_RELU>), grid, block,
                        0, stream, a);
   else if (a.act == ACT_GELU_ERF)
-    hipLaunchKernelGGL((gemm_skinny_stream_kernel<FP8, KW, KSM, NBUF, OUT, ACT_GELU_ERF>), grid,
+    hipLaunchKernelGGL((gemm_skinny_stream_kernel<TY, KW, KSM, NBUF, OUT, ACT_GELU_ERF>), grid,
                        block, 0, stream, a);
   else
-    hipLaunchKernelGGL((gemm_skinny_stream_kernel<FP8, KW, KSM, NBUF, OUT, ACT_GELU_TANH>), grid,
+    hipLaunchKernelGGL((gemm_skinny_stream_kernel<TY, KW, KSM, NBUF, OUT, ACT_GELU_TANH>), grid,
                        block, 0, stream, a);
   return hipGetLastError();
 }
 
-template <bool FP8>
+template <int TY>
 static hipError_t launch_stream(const GemmArgs& a, int out, hipStream_t stream) {
-  if (out == OUT_BF16) return launch_stream_out<FP8, OUT_BF16>(a, stream);
-  if (out == OUT_I8) return launch_stream_out<FP8, OUT_I8>(a, stream);
-  if (out == OUT_E4M3) return launch_stream_out<FP8, OUT_E4M3>(a, stream);
-  return launch_stream_out<FP8, OUT_F32>(a, stream);
+  if (out == OUT_BF16) return launch_stream_out<TY, OUT_BF16>(a, stream);
+  if (out == OUT_I8) return launch_stream_out<TY, OUT_I8>(a, stream);
+  if (out == OUT_E4M3) return launch_stream_out<TY, OUT_E4M3>(a, stream);
+  return launch_stream_out<TY, OUT_F32>(a, stream);
 }
 
 hipError_t launch_skinny(const Plan& plan, const LaunchSpec& spec, const GemmArgs& a,
@@ -385,10 +404,12 @@ hipError_t launch_skinny(const Plan& plan, const LaunchSpec& spec, const GemmArg
   (void)plan;
   if (a.M > 16) return hipErrorInvalidValue;  // the plan only selects M <= 16
   if (skinny_streams(a.K))
-    return spec.fp8 ? launch_stream<true>(a, spec.out, stream)
-                    : launch_stream<false>(a, spec.out, stream);
-  return spec.fp8 ? launch_mb<true, 1>(a, spec.out, stream)
-                  : launch_mb<false, 1>(a, spec.out, stream);
+    return spec.i8    ? launch_stream<TY_I8>(a, spec.out, stream)
+           : spec.fp8 ? launch_stream<TY_FP8>(a, spec.out, stream)
+                      : launch_stream<TY_BF16>(a, spec.out, stream);
+  return spec.i8    ? launch_mb<TY_I8, 1>(a, spec.out, stream)
+         : spec.fp8 ? launch_mb<TY_FP8, 1>(a, spec.out, stream)
+                    : launch_mb<TY_BF16, 1>(a, spec.out, stream);
 }
 #endif  // G355_KERNELS_ONLY
 

@@ -54,7 +54,7 @@ __device__ __forceinline__ int swz(int r) {
 }
 
 template <int BM_, int BN_, int WM_, int WN_, bool FP8_, int ROWB_, int STAGES_, int SPREAD_ = 1,
-          bool MX_ = false>
+          bool MX_ = false, bool I8_ = false>
 struct TileCfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ROWB = ROWB_, STAGES = STAGES_;
   // K-steps over which the global->LDS loads of one slice are issued.
@@ -64,9 +64,16 @@ struct TileCfg {
   // of B, applied by the MFMA itself (no FP32 per-row / per-column scales).
   static constexpr bool MX = MX_;
   static_assert(!MX || (FP8 && ROWB == 128), "MX scales: FP8 with four 32-element blocks per slice");
+  // INT8 operands, INT32 accumulators: bytes are laid out and scheduled as in
+  // the BF16 kernel (32 bytes of a row per MFMA), twice the elements per byte.
+  static constexpr bool I8 = I8_;
+  static_assert(!I8 || !FP8, "one element type");
+  // One FP32 scale per row of A and per column of B, applied in the epilogue.
+  static constexpr bool SCALED = (FP8 && !MX) || I8;
+  using Acc = std::conditional_t<I8, i32x16, f32x16>;
   static constexpr int NWAVES = WM * WN;
   static constexpr int NT = NWAVES * 64;
-  static constexpr int ES = FP8 ? 1 : 2;      // bytes per element
+  static constexpr int ES = FP8 || I8 ? 1 : 2;  // bytes per element
   static constexpr int CPR = ROWB / 16;       // 16-byte chunks per row
   static constexpr int BKE = ROWB / ES;       // K elements per slice
   static constexpr int CE = 16 / ES;          // K elements per chunk
@@ -78,7 +85,8 @@ struct TileCfg {
   static constexpr int WTN = BN / WN;
   static constexpr int FM = WTM / 32;         // 32x32 MFMA blocks per wave
   static constexpr int FN = WTN / 32;
-  // MFMA k-steps per slice: BF16 32x32x16 eats 32 B of a row, FP8 32x32x64 64 B.
+  // MFMA k-steps per slice: BF16 32x32x16 and INT8 32x32x32 eat 32 B of a row,
+  // FP8 32x32x64 64 B.
   static constexpr int KSTEPS = FP8 ? ROWB / 64 : ROWB / 32;
   static_assert(ROWB == 64 || ROWB == 128, "row bytes");
   static_assert(KSTEPS >= 1, "k steps");
@@ -210,6 +218,64 @@ struct NmajorLoader {
   }
 };
 
+// --------------------------------------------- DMA loader, rows of the K axis
+
+// Either operand of the weight gradient: the contraction runs over rows of
+// memory (tokens), COLS consecutive columns of which make a tile, BF16. Slices
+// land in the N-major LDS tile of NmajorLoader and are read by the same
+// transposing reads. Unlike there, rows may start at any 2-byte boundary and
+// the operand may be of any size: the descriptor's base moves with the slice
+// (64-bit scalar arithmetic), so a lane's offset stays below 64 rows, and its
+// range ends with the last row of the K range, so that rows past it read
+// zeros. A chunk that straddles the last column reads what follows the row
+// into columns that are never stored. The range check drops a 4-byte word
+// that lies partly past the range, which for an odd column count is the word
+// of the last element itself: the range is therefore 2 bytes longer (the
+// caller makes sure that those stay on the operand's last page).
+template <class C, int COLS, int NW = C::NWAVES>
+struct RowsLoader {
+  static constexpr int ROWN = COLS * 2;
+  static constexpr int CPRN = ROWN / 16;
+  static constexpr int RPSN = 1024 / ROWN;
+  static constexpr int SEGS = C::BKE / RPSN;
+  static constexpr int IPW = SEGS / NW;
+  static constexpr uint32_t kNowhere = 0x80000000u;  // past every range
+  uint32_t off[IPW];
+  const char* base;
+  int64_t ld2;  // bytes per row
+  int cols;
+
+  __device__ __forceinline__ void init(const void* ptr, int64_t ld, int col0, int cols_, int wave,
+                                       int lane) {
+    base = static_cast<const char*>(ptr);
+    ld2 = ld * 2;
+    cols = cols_;
+#pragma unroll
+    for (int i = 0; i < IPW; ++i) {
+      const int r = (wave * IPW + i) * RPSN + lane / CPRN;
+      const int lc = (lane % CPRN) ^ (4 * (r & 3));
+      const int n = col0 + 8 * lc;
+      off[i] = n < cols ? static_cast<uint32_t>(r * ld2 + n * 2) : kNowhere;
+    }
+  }
+
+  template <int I0 = 0, int I1 = IPW>
+  __device__ __forceinline__ void issue_buf(char* lds_tile, int wave, __amdgpu_buffer_rsrc_t,
+                                            int koff, uint32_t oob, int k0, int k_end,
+                                            bool full) const {
+    (void)koff, (void)oob, (void)full;
+    const int rem = k_end - k0;
+    const int64_t want = rem > 0 ? (rem - 1) * ld2 + cols * 2 + 2 : 0;
+    const int range = static_cast<int>(want < INT32_MAX ? want : INT32_MAX);
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(base + k0 * ld2), 0, range, kBufferWord3);
+#pragma unroll
+    for (int i = I0; i < I1; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (G355_LDS void*)(lds_tile + (wave * IPW + i) * 1024),
+                                               16, static_cast<int>(off[i]), 0, 0, 0);
+  }
+};
+
 // ------------------------------------------------------------- register loader
 
 template <class C, int ROWS>
@@ -269,8 +335,9 @@ struct GenericLoader {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-template <bool FP8> struct FragOf { using type = bf16x8; };   // 8 BF16: one ds_read_b128
-template <> struct FragOf<true> { using type = i32x8; };     // 32 FP8: two ds_read_b128
+// One MFMA's operand in a lane: 8 BF16 or 16 INT8 (one ds_read_b128), or 32 FP8 (two).
+template <class C>
+using FragOf = std::conditional_t<C::FP8, i32x8, std::conditional_t<C::I8, i32x4, bf16x8>>;
 
 // Wait until at most N of this wave's global loads are outstanding and all of
 // its LDS operations are done, then barrier. (N is the number of loads of
@@ -345,6 +412,11 @@ struct DmaPart {
 
 // ------------------------------------------------------------------ epilogue
 
+// An accumulator element as the 32 bits that pass through LDS and the split-K
+// workspace: FP32, or an INT32 sum unchanged.
+__device__ __forceinline__ float acc_bits(float v) { return v; }
+__device__ __forceinline__ float acc_bits(int v) { return __int_as_float(v); }
+
 // Output tile epilogue for one wave, staged through LDS so that global C
 // traffic is row-contiguous: the wave writes one 32-row strip of its
 // accumulators (all FN column blocks) into a private LDS area, then reads it
@@ -366,8 +438,8 @@ struct EpiLayout {
 };
 
 template <class C, int OUT, bool SPLIT, int ACT>
-__device__ __forceinline__ void epilogue(const GemmArgs& p, const f32x16 (&acc)[C::FM][C::FN],
-                                         float* lds, int row0, int col0, int lane, int split) {
+__device__ __forceinline__ void epilogue(const GemmArgs& p,
+                                         const typename C::Acc (&acc)[C::FM][C::FN], float* lds, int row0, int col0, int lane, int split) {
   using E = EpiLayout<C>;
   const int M = p.M, N = p.N;
   const int half = lane >> 5;
@@ -385,10 +457,19 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const f32x16 (&acc)[
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (n + q < N) {
-        if constexpr (C::FP8 && !C::MX) cs[q] = p.alpha * p.scale_b[n + q];
+        if constexpr (C::SCALED) cs[q] = p.alpha * p.scale_b[n + q];
         if (p.bias) bias_v[q] = bf16_bits_to_f32(p.bias[n + q]);
       }
     }
+  }
+
+  // INT8 with a zero point per row: the columns' sums of B (0 without).
+  const bool has_zero = C::I8 && !SPLIT && p.zero_a != nullptr;
+  double cz[4] = {0.0, 0.0, 0.0, 0.0};
+  if (has_zero) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (n + q < N) cz[q] = static_cast<double>(p.sum_b[n + q]);
   }
 
   // C_in of strip i+1 is requested before strip i is processed, so its HBM
@@ -447,11 +528,12 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const f32x16 (&acc)[
   // holds rows l and 64 + l. A row's value is later taken from its lane with
   // a cross-lane read, so no global load (and no wait on one, which on this
   // chip would also wait for every earlier store) sits inside the row loop.
-  constexpr bool ROW_SA = !SPLIT && C::FP8 && !C::MX;
+  constexpr bool ROW_SA = !SPLIT && C::SCALED;
   constexpr bool ROW_QS = !SPLIT && OUT >= OUT_I8;
   constexpr bool ROW_QZ = !SPLIT && OUT == OUT_I8;
   constexpr int RREG = (32 * C::FM + 63) / 64;
   float row_sa[RREG], row_qs[RREG], row_qz[RREG];
+  int row_za[RREG];
 #pragma unroll
   for (int j = 0; j < RREG; ++j) {
     const int lr = 64 * j + lane;
@@ -460,9 +542,11 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const f32x16 (&acc)[
     row_sa[j] = 1.f;
     row_qs[j] = 1.f;
     row_qz[j] = 0.f;
+    row_za[j] = 0;
     if constexpr (ROW_SA) {
       if (ok) row_sa[j] = p.scale_a[m];
     }
+    if (has_zero && ok) row_za[j] = p.zero_a[m];
     if constexpr (ROW_QS) {
       if (ok) row_qs[j] = p.qscale[m];
     }
@@ -485,7 +569,8 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const f32x16 (&acc)[
     for (int j = 0; j < C::FN; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e)
-        lds[(8 * (e >> 2) + 4 * half + (e & 3)) * E::STR + 32 * j + (lane & 31)] = acc[i][j][e];
+        lds[(8 * (e >> 2) + 4 * half + (e & 3)) * E::STR + 32 * j + (lane & 31)] =
+            acc_bits(acc[i][j][e]);
 
 #pragma unroll
     for (int it = 0; it < E::ITERS; ++it) {
@@ -500,8 +585,14 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const f32x16 (&acc)[
       if constexpr (ROW_SA) sa = __shfl(row_sa[i >> 1], src);
       if constexpr (ROW_QS) qs = __shfl(row_qs[i >> 1], src);
       if constexpr (ROW_QZ) qz = __shfl(row_qz[i >> 1], src);
+      int za = 0;
+      if (has_zero) za = __shfl(row_za[i >> 1], src);
       if (m >= M) continue;
       float v[4] = {a4.x, a4.y, a4.z, a4.w};
+      if constexpr (C::I8 && !SPLIT) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = i8_sum(__float_as_int(v[q]), has_zero, za, cz[q]);
+      }
       if constexpr (SPLIT) {
         // Partials are written once and read once by the reduction: non-temporal.
         float* w = p.workspace + (static_cast<int64_t>(split) * M + m) * N + n;
@@ -559,8 +650,8 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, const f32x16 (&acc)[
 
 // Runs the epilogue with the activation as a compile-time parameter.
 template <class C, int OUT, bool SPLIT>
-__device__ __forceinline__ void run_epilogue(const GemmArgs& p, const f32x16 (&acc)[C::FM][C::FN],
-                                             float* lds, int row0, int col0, int lane, int split) {
+__device__ __forceinline__ void run_epilogue(const GemmArgs& p,
+                                             const typename C::Acc (&acc)[C::FM][C::FN], float* lds, int row0, int col0, int lane, int split) {
   if constexpr (SPLIT) {
     epilogue<C, OUT, true, ACT_NONE>(p, acc, lds, row0, col0, lane, split);
   } else {
@@ -576,12 +667,74 @@ __device__ __forceinline__ void run_epilogue(const GemmArgs& p, const f32x16 (&a
   }
 }
 
+// ------------------------------------------------------- products grouped by rows
+
+// MODE_GROUPED: rows offsets[g] .. offsets[g+1]-1 of A and C belong to group
+// g, which has a B (bias, scale_b, sum_b) of its own. MODE_WGRAD: C of group g
+// is the product of two operands over those rows (their contraction axis).
+enum TileMode : int { MODE_DENSE = 0, MODE_GROUPED = 1, MODE_WGRAD = 2 };
+
+// Group g's rows [s, e). The offsets are device data that no host check has
+// seen: clamped here, so that whatever they hold no access leaves the arrays.
+__device__ __forceinline__ void group_rows(const GemmArgs& p, int g, int& s, int& e) {
+  s = min(max(p.offsets[g], 0), p.rows_total);
+  e = min(max(p.offsets[g + 1], s), p.rows_total);
+}
+
+// The row tile of workgroup `b`: every wave counts the row tiles of all groups
+// (64 groups at a time, one per lane) and finds its own in their running sum,
+// so the launch needs neither a host copy of the offsets nor a kernel before
+// it. The grid is the largest count possible; workgroups past the real one
+// (nwg) return, and the real ones are spread over the XCDs evenly.
+// tiles: row tiles of the found group; first: row tiles of the groups before it.
+template <int BM>
+__device__ __forceinline__ bool find_group(const GemmArgs& p, int b, int lane, int& L, int& g,
+                                           int& s, int& rows, int& tiles, int& first) {
+  const auto count = [&](int c, int& gs, int& ge) {
+    gs = ge = 0;
+    if (c + lane < p.groups) group_rows(p, c + lane, gs, ge);
+    return (ge - gs + BM - 1) / BM;
+  };
+  const auto running_sum = [&](int n) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int t = __shfl_up(n, o);
+      n += lane >= o ? t : 0;
+    }
+    return n;
+  };
+  int gs, ge, total = 0;
+  for (int c = 0; c < p.groups; c += 64) total += __shfl(running_sum(count(c, gs, ge)), 63);
+  total = __builtin_amdgcn_readfirstlane(total);
+  const int nwg = total * p.tiles_n;
+  if (b >= nwg) return false;
+  L = xcd_remap(b, nwg);
+  const int rt = L / p.tiles_n;
+  int before = 0;
+  for (int c = 0; c < p.groups; c += 64) {
+    const int n = count(c, gs, ge);
+    const int incl = running_sum(n);
+    const unsigned long long hit = __ballot(before + incl > rt);
+    if (hit != 0) {
+      const int src = __builtin_ctzll(hit);
+      g = c + src;
+      s = __builtin_amdgcn_readlane(gs, src);
+      rows = __builtin_amdgcn_readlane(ge, src) - s;
+      tiles = __builtin_amdgcn_readlane(n, src);
+      first = before + __builtin_amdgcn_readlane(incl, src) - tiles;
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return false;  // not reached: rt < total
+}
+
 // ------------------------------------------------------------------- the kernel
 
 // RAGGED: K may end inside a 16-byte chunk of a DMA-fed row (patch_tail).
 // Kept out of the other instantiations: the patch's code perturbs the
 // register allocation of the K loop.
-template <class C, int LA, int LB, int OUT, bool SPLIT, bool RAGGED>
+template <class C, int LA, int LB, int OUT, bool SPLIT, bool RAGGED, int MODE = MODE_DENSE>
 __global__ void __launch_bounds__(C::NT)
 gemm_tile_kernel(GemmArgs p) {
   // The LDS block holds the ring of K slices, and after the main loop the
@@ -596,11 +749,58 @@ gemm_tile_kernel(GemmArgs p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
   // ---- which tile and which K range
-  const int tiles = p.tiles_m * p.tiles_n;
-  const int L = xcd_remap(blockIdx.x, gridDim.x);
-  const int split = L / tiles;
-  int tm, tn;
-  tile_coords(L - split * tiles, p.tiles_m, p.tiles_n, 4, tm, tn);
+  int tm, tn, split = 0;
+  if constexpr (MODE == MODE_DENSE) {
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int L = xcd_remap(blockIdx.x, gridDim.x);
+    split = L / tiles;
+    tile_coords(L - split * tiles, p.tiles_m, p.tiles_n, 4, tm, tn);
+  } else if constexpr (MODE == MODE_GROUPED) {
+    int L, g, s, rows, tiles, first;
+    if (!find_group<C::BM>(p, blockIdx.x, lane, L, g, s, rows, tiles, first)) return;
+    tile_coords(L - first * p.tiles_n, tiles, p.tiles_n, 4, tm, tn);
+    // The operands of this row tile alone, its first row as row 0: 64-bit
+    // pointer arithmetic here, so that the kernel's 32-bit offsets never see
+    // more than a tile's rows or one group's weight.
+    const int r0 = s + tm * C::BM;
+    p.A = static_cast<const char*>(p.A) + r0 * p.lda * C::ES;
+    p.C = static_cast<char*>(p.C) + r0 * p.ldc * (OUT == OUT_F32 ? 4 : 2);
+    p.M = min(rows - tm * C::BM, C::BM);
+    tm = 0;
+    p.B = static_cast<const char*>(p.B) + g * p.stride_b * C::ES;
+    const int64_t gn = static_cast<int64_t>(g) * p.N;
+    if (p.bias) p.bias += gn;
+    if constexpr (C::SCALED) {
+      p.scale_a += r0;
+      p.scale_b += gn;
+      if (p.zero_a) {
+        p.zero_a += r0;
+        p.sum_b += gn;
+      }
+    }
+  } else {
+    // Every group has the same tiles; the groups differ in their K range. Each
+    // XCD takes an eighth of every group's tiles, neighbours of each other, so
+    // that groups of unequal length load the XCDs alike.
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int b = blockIdx.x;
+    int g = b / tiles, t = b - g * tiles;
+    if (tiles >= kWgradXcdTiles) {
+      const int per = (tiles + 7) / 8;
+      g = (b >> 3) / per;
+      t = (b & 7) * per + (b >> 3) - g * per;
+      if (t >= tiles) return;
+    }
+    tile_coords(t, p.tiles_m, p.tiles_n, 4, tm, tn);
+    int s, e;
+    group_rows(p, g, s, e);
+    p.K = __builtin_amdgcn_readfirstlane(e - s);
+    s = __builtin_amdgcn_readfirstlane(s);
+    p.A = static_cast<const char*>(p.A) + s * p.lda * C::ES;
+    p.B = static_cast<const char*>(p.B) + s * p.ldb * C::ES;
+    p.C = static_cast<char*>(p.C) + g * p.stride_b * (OUT == OUT_F32 ? 4 : 2);
+    p.k_split_len = p.K;
+  }
   const int m0 = tm * C::BM, n0 = tn * C::BN;
   const int k_begin = split * p.k_split_len;
   const int k_end = min(p.K, k_begin + p.k_split_len);
@@ -616,10 +816,14 @@ gemm_tile_kernel(GemmArgs p) {
   DirectLoader<C, C::BN, C::NWAVES, (C::BM == 64 ? kPolicyNonTemporal : 0)> db;
   using NLoader = NmajorLoader<C>;
   NLoader dn;
+  RowsLoader<C, C::BM> ra;
+  RowsLoader<C, C::BN> rb;
   GenericLoader<C, C::BM> ga;
   GenericLoader<C, C::BN> gb;
   if constexpr (LA == LOAD_DIRECT) {
     da.init(p.lda, m0, p.M, wave, lane);
+  } else if constexpr (LA == LOAD_ROWS) {
+    ra.init(p.A, p.lda, m0, p.M, wave, lane);
   } else {
     ga.base = static_cast<const char*>(p.A); ga.ld = p.lda; ga.row0 = m0; ga.rows = p.M;
     ga.kmajor = p.a_mn_major == 0;
@@ -629,8 +833,11 @@ gemm_tile_kernel(GemmArgs p) {
   // into range).
   const uint32_t ext_a = static_cast<uint32_t>(
       (static_cast<int64_t>(p.M - 1) * p.lda + p.K) * C::ES);
+  // (Two bytes more for a group's N-major weight, whose column count may be
+  // odd: see RowsLoader.)
   const uint32_t ext_b = static_cast<uint32_t>(
-      LB == LOAD_DIRECT_N ? (static_cast<int64_t>(p.K - 1) * p.ldb + p.N) * C::ES
+      LB == LOAD_DIRECT_N ? (static_cast<int64_t>(p.K - 1) * p.ldb + p.N) * C::ES +
+                                (MODE == MODE_GROUPED ? 2 : 0)
                           : (static_cast<int64_t>(p.N - 1) * p.ldb + p.K) * C::ES);
   const __amdgpu_buffer_rsrc_t rsrc_a = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<void*>(p.A), 0, static_cast<int>(ext_a), kBufferWord3);
@@ -640,14 +847,20 @@ gemm_tile_kernel(GemmArgs p) {
     db.init(p.ldb, n0, p.N, wave, lane);
   } else if constexpr (LB == LOAD_DIRECT_N) {
     dn.init(p.ldb, n0, p.N, ext_b, wave, lane);
+  } else if constexpr (LB == LOAD_ROWS) {
+    rb.init(p.B, p.ldb, n0, p.N, wave, lane);
   } else {
     gb.base = static_cast<const char*>(p.B); gb.ld = p.ldb; gb.row0 = n0; gb.rows = p.N;
     gb.kmajor = p.b_mn_major == 0;
   }
-  constexpr int DMA_PER_SLICE = (LA == LOAD_DIRECT ? DirectLoader<C, C::BM>::IPW : 0) +
-                                (LB == LOAD_DIRECT     ? DirectLoader<C, C::BN>::IPW
-                                 : LB == LOAD_DIRECT_N ? NLoader::IPW
-                                                       : 0);
+  constexpr int NA = LA == LOAD_DIRECT ? DirectLoader<C, C::BM>::IPW
+                     : LA == LOAD_ROWS ? RowsLoader<C, C::BM>::IPW
+                                       : 0;
+  constexpr int NB = LB == LOAD_DIRECT     ? DirectLoader<C, C::BN>::IPW
+                     : LB == LOAD_DIRECT_N ? NLoader::IPW
+                     : LB == LOAD_ROWS     ? RowsLoader<C, C::BN>::IPW
+                                           : 0;
+  constexpr int DMA_PER_SLICE = NA + NB;
   // At boundary j the loads of slice j+1 must be complete; those of slices
   // j+2 .. j+STAGES-1 (issued at the STAGES-2 boundaries before) may still
   // be in flight. Register-loaded slices are already in LDS by then.
@@ -660,11 +873,15 @@ gemm_tile_kernel(GemmArgs p) {
     const bool full = k0 + C::BKE <= k_end;
     if constexpr (LA == LOAD_DIRECT)
       da.issue_buf(a_tile(st), wave, rsrc_a, k0 * C::ES, ext_a, k0, k_end, full);
+    else if constexpr (LA == LOAD_ROWS)
+      ra.issue_buf(a_tile(st), wave, rsrc_a, 0, 0, k0, k_end, full);
     else ga.load(tid, k0, k_end);
     if constexpr (LB == LOAD_DIRECT)
       db.issue_buf(b_tile(st), wave, rsrc_b, k0 * C::ES, ext_b, k0, k_end, full);
     else if constexpr (LB == LOAD_DIRECT_N)
       dn.issue_buf(b_tile(st), wave, rsrc_b, 0, ext_b, k0, k_end, full);
+    else if constexpr (LB == LOAD_ROWS)
+      rb.issue_buf(b_tile(st), wave, rsrc_b, 0, 0, k0, k_end, full);
     else gb.load(tid, k0, k_end);
   };
   auto commit = [&](int st) __attribute__((always_inline)) {
@@ -734,27 +951,44 @@ gemm_tile_kernel(GemmArgs p) {
   // read at row (j / 4) of a 4-row band and columns 4*(j % 4) .. +3 of the
   // group's 16 columns; lane i then receives column i of the 4 rows. kq =
   // (lane%16)/4 is the lane's row in the band, so its chunks are XORed with 4*kq.
+  // (An N-major A, in the weight gradient, is read the same way.)
+  constexpr bool A_ROWS = LA == LOAD_ROWS;
+  constexpr bool B_ROWS = LB == LOAD_DIRECT_N || LB == LOAD_ROWS;
+  constexpr int ROWN_A = C::BM * 2, ROWN_B = C::BN * 2;  // bytes per LDS row of such a tile
   int ntr_row = 0, ntr_col[C::FN];
-  if constexpr (LB == LOAD_DIRECT_N) {
+  int atr_row = 0, atr_col[C::FM];
+  if constexpr (A_ROWS || B_ROWS) {
     const int kq = (lane & 15) >> 2;
-    ntr_row = (8 * half + kq) * NLoader::ROWN + 8 * (lane & 1);
+    ntr_row = (8 * half + kq) * ROWN_B + 8 * (lane & 1);
+    atr_row = (8 * half + kq) * ROWN_A + 8 * (lane & 1);
     const int lc0 = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
 #pragma unroll
     for (int j = 0; j < C::FN; ++j)
       ntr_col[j] = ((((wn0 + 32 * j) >> 3) ^ (4 * kq)) + lc0) << 4;
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+      atr_col[i] = ((((wm0 + 32 * i) >> 3) ^ (4 * kq)) + lc0) << 4;
   }
+  // k rows 16t + 8*half + 0..7 of the lane's column, as two transposing reads
+  // of four rows each (rows 16t + 8*half + 4r + kq, kq = (lane%16)/4). `q`: the
+  // lane's address of the first.
+  auto read_tr = [&](const char* q, int rown) __attribute__((always_inline)) {
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((G355_LDS s16x4*)(q));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((G355_LDS s16x4*)(q + 4 * rown));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
 
-  f32x16 acc[C::FM][C::FN];
+  typename C::Acc acc[C::FM][C::FN];
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
     for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
   // Fragment registers: two sets, so that the reads of the next k-step go to
   // one set while the MFMAs of the current k-step consume the other.
-  using Frag = typename FragOf<C::FP8>::type;
+  using Frag = FragOf<C>;
   Frag fa0[C::FM], fb0[C::FN], fa1[C::FM], fb1[C::FN];
 
   // LDS -> registers: the fragments of k-step t of the slice in stage st.
@@ -764,23 +998,22 @@ gemm_tile_kernel(GemmArgs p) {
     if constexpr (!C::FP8) {
       const int co = ((2 * t + half) ^ sw) << 4;
 #pragma unroll
-      for (int i = 0; i < C::FM; ++i)
-        fa[i] = *reinterpret_cast<const bf16x8*>(at + a_row + i * 32 * C::ROWB + co);
-      if constexpr (LB == LOAD_DIRECT_N) {
-        // k rows 16t + 8*half + 0..7 of the lane's column, as two transposing
-        // reads of four rows each (rows 16t + 8*half + 4r + kq, kq = (lane%16)/4).
+      for (int i = 0; i < C::FM; ++i) {
+        if constexpr (A_ROWS)
+          fa[i] = __builtin_bit_cast(
+              Frag, read_tr(at + atr_row + atr_col[i] + (16 * t) * ROWN_A, ROWN_A));
+        else
+          fa[i] = *reinterpret_cast<const Frag*>(at + a_row + i * 32 * C::ROWB + co);
+      }
+      if constexpr (B_ROWS) {
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j) {
-          const char* q = bt + ntr_row + ntr_col[j] + (16 * t) * NLoader::ROWN;
-          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((G355_LDS s16x4*)(q));
-          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (G355_LDS s16x4*)(q + 4 * NLoader::ROWN));
-          fb[j] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        }
+        for (int j = 0; j < C::FN; ++j)
+          fb[j] = __builtin_bit_cast(
+              Frag, read_tr(bt + ntr_row + ntr_col[j] + (16 * t) * ROWN_B, ROWN_B));
       } else {
 #pragma unroll
         for (int j = 0; j < C::FN; ++j)
-          fb[j] = *reinterpret_cast<const bf16x8*>(bt + b_row + j * 32 * C::ROWB + co);
+          fb[j] = *reinterpret_cast<const Frag*>(bt + b_row + j * 32 * C::ROWB + co);
       }
     } else {
       // Registers 0-3 and 4-7 of a lane take two 16-byte chunks of its row.
@@ -833,6 +1066,8 @@ gemm_tile_kernel(GemmArgs p) {
         else if constexpr (C::FP8)
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[i], fb[j], acc[i][j], 0,
                                                                      0, 0, 127, 0, 127);
+        else if constexpr (C::I8)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
         else
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
       }
@@ -855,18 +1090,13 @@ gemm_tile_kernel(GemmArgs p) {
   // in registers and write it to LDS just before boundary j+1.
   // LDS fragment reads per k-step (an N-major B block takes two 8-byte
   // transposing reads).
-  constexpr int READS = C::FP8              ? 2 * (C::FM + C::FN)
-                        : LB == LOAD_DIRECT_N ? C::FM + 2 * C::FN
-                                              : C::FM + C::FN;
+  constexpr int READS =
+      C::FP8 ? 2 * (C::FM + C::FN) : (A_ROWS ? 2 : 1) * C::FM + (B_ROWS ? 2 : 1) * C::FN;
   constexpr int MFMAS = C::FM * C::FN;
-  constexpr bool ALL_DMA = LA == LOAD_DIRECT && (LB == LOAD_DIRECT || LB == LOAD_DIRECT_N);
+  constexpr bool ALL_DMA = LA != LOAD_GENERIC && LB != LOAD_GENERIC;
   // With both operands on the DMA path, the loads of slice s are issued in
   // SPREAD parts: part 0 at boundary s-STAGES, part p in the (p-1)-th k-step
   // after it, so that the loads of all waves do not queue up at once.
-  constexpr int NA = LA == LOAD_DIRECT ? DirectLoader<C, C::BM>::IPW : 0;
-  constexpr int NB = LB == LOAD_DIRECT     ? DirectLoader<C, C::BN>::IPW
-                     : LB == LOAD_DIRECT_N ? NLoader::IPW
-                                           : 0;
   using Part0 = DmaPart<C, NA, NB, 0>;
   using Part1 = DmaPart<C, NA, NB, 1>;
   using Part2 = DmaPart<C, NA, NB, 2>;
@@ -875,7 +1105,9 @@ gemm_tile_kernel(GemmArgs p) {
     using Pt = decltype(part);
     const int k0 = k_begin + s * C::BKE;
     const int st = s % C::STAGES;
-    if constexpr (LB == LOAD_DIRECT_N)
+    if constexpr (LA == LOAD_ROWS)
+      Pt::issue(ra, rb, a_tile(st), b_tile(st), wave, rsrc_a, rsrc_b, 0, 0, 0, k0, k_end, false);
+    else if constexpr (LB == LOAD_DIRECT_N)
       Pt::issue(da, dn, a_tile(st), b_tile(st), wave, rsrc_a, rsrc_b, ext_a, ext_b, k0 * C::ES,
                 k0, k_end, k0 + C::BKE <= k_end);
     else
@@ -1025,7 +1257,31 @@ gemm_tile_kernel(GemmArgs p) {
 // ----------------------------------------------------------- split-K reduction
 
 // C = epilogue(sum over splits s = 0..S-1, in that order, of workspace[s]).
-template <bool FP8, int OUT>
+// The partials are FP32, or INT32 bits for INT8 operands (TY), whose sum is exact.
+enum ReduceType : int { RED_PLAIN = 0, RED_FP8 = 1, RED_I8 = 2 };
+
+// Sum of the partials of one element in split order.
+template <int TY>
+__device__ __forceinline__ float add_partials(const GemmArgs& p, const float (&part)[kMaxSplit],
+                                              int m, int n) {
+  if constexpr (TY == RED_I8) {
+    int v = 0;
+#pragma unroll
+    for (int s = 0; s < kMaxSplit; ++s)
+      if (s < p.split_k) v += __float_as_int(part[s]);
+    const bool has_zero = p.zero_a != nullptr;
+    return i8_sum(v, has_zero, has_zero ? p.zero_a[m] : 0,
+                  has_zero ? static_cast<double>(p.sum_b[n]) : 0.0);
+  } else {
+    float v = 0.f;
+#pragma unroll
+    for (int s = 0; s < kMaxSplit; ++s)
+      if (s < p.split_k) v += part[s];
+    return v;
+  }
+}
+
+template <int TY, int OUT>
 __global__ void __launch_bounds__(256) splitk_reduce_kernel(GemmArgs p) {
   const int64_t MN = static_cast<int64_t>(p.M) * p.N;
   const int64_t idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -1039,11 +1295,8 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(GemmArgs p) {
 #pragma unroll
   for (int s = 0; s < kMaxSplit; ++s)
     if (s < p.split_k) part[s] = __builtin_nontemporal_load(p.workspace + s * MN + idx);
-  float v = 0.f;
-#pragma unroll
-  for (int s = 0; s < kMaxSplit; ++s)
-    if (s < p.split_k) v += part[s];
-  if constexpr (FP8) v = v * (p.scale_a[m] * p.scale_b[n]);
+  float v = add_partials<TY>(p, part, m, n);
+  if constexpr (TY != RED_PLAIN) v = v * (p.scale_a[m] * p.scale_b[n]);
   v = p.alpha * v;
   const int64_t off = static_cast<int64_t>(m) * p.ldc + n;
   if constexpr (OUT == OUT_F32 || OUT == OUT_BF16) {
@@ -1059,7 +1312,7 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(GemmArgs p) {
 // The same, four consecutive elements of one row per thread (N and ldc
 // multiples of 4, workspace and C 16-byte aligned): 16-byte partial loads and
 // one vector store. The per-element arithmetic is the scalar kernel's.
-template <bool FP8, int OUT>
+template <int TY, int OUT>
 __global__ void __launch_bounds__(256) splitk_reduce4_kernel(GemmArgs p) {
   const int64_t MN = static_cast<int64_t>(p.M) * p.N;
   const int64_t idx = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
@@ -1071,17 +1324,19 @@ __global__ void __launch_bounds__(256) splitk_reduce4_kernel(GemmArgs p) {
   for (int s = 0; s < kMaxSplit; ++s)
     if (s < p.split_k)
       part[s] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p.workspace + s * MN + idx));
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  float v[4];
 #pragma unroll
-  for (int s = 0; s < kMaxSplit; ++s)
-    if (s < p.split_k) {
+  for (int q = 0; q < 4; ++q) {
+    float one[kMaxSplit];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] += part[s][q];
-    }
+    for (int s = 0; s < kMaxSplit; ++s)
+      if (s < p.split_k) one[s] = part[s][q];
+    v[q] = add_partials<TY>(p, one, m, n + q);
+  }
   const int64_t off = static_cast<int64_t>(m) * p.ldc + n;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    if constexpr (FP8) v[q] = v[q] * (p.scale_a[m] * p.scale_b[n + q]);
+    if constexpr (TY != RED_PLAIN) v[q] = v[q] * (p.scale_a[m] * p.scale_b[n + q]);
     v[q] = p.alpha * v[q];
     if constexpr (OUT == OUT_F32 || OUT == OUT_BF16) {
       if (p.beta != 0.f) v[q] += p.beta * load_cin1<OUT>(p.C, off + q);
@@ -1099,15 +1354,27 @@ __global__ void __launch_bounds__(256) splitk_reduce4_kernel(GemmArgs p) {
 // This file is compiled once per (ragged, output part) pair, with G355_PART
 // (an OutPart) and G355_RAGGED (0 or 1) defined, and once with G355_REDUCE
 // for the split-K reduction: each compile instantiates only the kernels of its
-// output kind, so the kernel variants build in parallel.
+// output kind, so the kernel variants build in parallel. G355_I8, G355_GROUPED
+// and G355_WGRAD select the INT8 kernels, the grouped products and their
+// weight gradient instead of the dense BF16 and FP8 kernels.
 #if defined(G355_PART)
+
+constexpr int PART = G355_PART;
+
+// The tile kernel of this part's output kind.
+template <class C, int LA, int LB, bool RAGGED, int MODE>
+static hipError_t launch_grouped(int64_t grid, const GemmArgs& a, hipStream_t stream) {
+  constexpr int OUT = PART == PART_F32 ? OUT_F32 : OUT_BF16;
+  hipLaunchKernelGGL((gemm_tile_kernel<C, LA, LB, OUT, false, RAGGED, MODE>),
+                     dim3(static_cast<unsigned>(grid)), dim3(C::NT), 0, stream, a);
+  return hipGetLastError();
+}
 
 template <class C, int LA, int LB, bool RAGGED, bool QUANT_OUT = true>
 static hipError_t launch_cfg(const Plan& plan, const LaunchSpec& spec, const GemmArgs& a,
                              hipStream_t stream) {
   (void)spec;
   const dim3 grid(static_cast<unsigned>(plan.grid)), block(C::NT);
-  constexpr int PART = G355_PART;
   if constexpr (PART == PART_SPLIT) {
     hipLaunchKernelGGL((gemm_tile_kernel<C, LA, LB, OUT_F32, true, RAGGED>), grid, block, 0,
                        stream, a);
@@ -1154,6 +1421,75 @@ using Thin8X = TileCfg<64, 256, 1, 4, true, 128, 4, 1, true>;
 using Narrow16 = TileCfg<64, 128, 1, 2, false, 128, 6>;
 using Narrow8 = TileCfg<64, 128, 1, 2, true, 128, 6>;
 using Narrow8X = TileCfg<64, 128, 1, 2, true, 128, 6, 1, true>;
+// INT8: BF16's schedules (a slice is the same bytes and the same MFMAs).
+template <int BM, int BN, int WM, int WN, int STAGES, int SPREAD = 1>
+using CfgI8 = TileCfg<BM, BN, WM, WN, false, 128, STAGES, SPREAD, false, true>;
+using BigI8 = CfgI8<256, 256, 2, 4, 2, 3>;
+using SmallI8 = CfgI8<128, 128, 2, 2, 2>;
+using ThinI8 = CfgI8<64, 256, 1, 4, 4>;
+using NarrowI8 = CfgI8<64, 128, 1, 2, 6>;
+
+#if defined(G355_I8)
+
+hipError_t G355_I8_LAUNCHER(G355_RAGGED, G355_PART)(const Plan& plan, const LaunchSpec& spec,
+                                                    const GemmArgs& a, hipStream_t stream) {
+  constexpr bool R = G355_RAGGED != 0;
+  if (spec.loader_a != LOAD_DIRECT || spec.loader_b != LOAD_DIRECT) {
+    // Register loading (an operand of 2 GiB or more) bounds every element: no ragged variant.
+    if constexpr (R) return hipErrorInvalidValue;
+    else return launch_cfg<SmallI8, LOAD_GENERIC, LOAD_GENERIC, R>(plan, spec, a, stream);
+  }
+  if (plan.bm == 64)
+    return plan.bn == 256 ? launch_cfg<ThinI8, LOAD_DIRECT, LOAD_DIRECT, R>(plan, spec, a, stream)
+                          : launch_cfg<NarrowI8, LOAD_DIRECT, LOAD_DIRECT, R>(plan, spec, a, stream);
+  return plan.bm == 256 ? launch_cfg<BigI8, LOAD_DIRECT, LOAD_DIRECT, R>(plan, spec, a, stream)
+                        : launch_cfg<SmallI8, LOAD_DIRECT, LOAD_DIRECT, R>(plan, spec, a, stream);
+}
+
+#elif defined(G355_GROUPED)
+
+// One element type's tiles: 256x256, 128x128, and 64x128 with a deep ring.
+template <class BIG, class SMALL, class NARROW, int LB>
+static hipError_t launch_grouped_type(const GroupedPlan& plan, const GemmArgs& a,
+                                      hipStream_t stream) {
+  constexpr bool R = G355_RAGGED != 0;
+  if (plan.bm == 256) return launch_grouped<BIG, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
+  if (plan.bm == 64) return launch_grouped<NARROW, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
+  return launch_grouped<SMALL, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
+}
+
+hipError_t G355_GROUPED_LAUNCHER(G355_RAGGED, G355_PART)(const GroupedPlan& plan,
+                                                         const LaunchSpec& spec, const GemmArgs& a,
+                                                         hipStream_t stream) {
+  if (spec.loader_b == LOAD_GENERIC) {
+    // Register loading of both operands, on the 128x128 tile.
+    if constexpr (G355_RAGGED != 0) return hipErrorInvalidValue;
+    else if (spec.i8)
+      return launch_grouped<SmallI8, LOAD_GENERIC, LOAD_GENERIC, false, MODE_GROUPED>(plan.grid, a, stream);
+    else if (spec.fp8)
+      return launch_grouped<Small8, LOAD_GENERIC, LOAD_GENERIC, false, MODE_GROUPED>(plan.grid, a, stream);
+    else
+      return launch_grouped<Small16, LOAD_GENERIC, LOAD_GENERIC, false, MODE_GROUPED>(plan.grid, a, stream);
+  }
+  if (spec.i8) return launch_grouped_type<BigI8, SmallI8, NarrowI8, LOAD_DIRECT>(plan, a, stream);
+  if (spec.fp8) return launch_grouped_type<Big8, Small8, Narrow8, LOAD_DIRECT>(plan, a, stream);
+  if (spec.loader_b == LOAD_DIRECT_N)
+    return launch_grouped_type<Big16, Small16, Narrow16, LOAD_DIRECT_N>(plan, a, stream);
+  return launch_grouped_type<Big16, Small16, Narrow16, LOAD_DIRECT>(plan, a, stream);
+}
+
+#elif defined(G355_WGRAD)
+
+hipError_t G355_WGRAD_LAUNCHER(G355_PART)(const GroupedPlan& plan, const LaunchSpec& spec,
+                                          const GemmArgs& a, hipStream_t stream) {
+  if (spec.loader_a == LOAD_GENERIC)
+    return launch_grouped<Small16, LOAD_GENERIC, LOAD_GENERIC, false, MODE_WGRAD>(plan.grid, a, stream);
+  if (plan.bm == 256)
+    return launch_grouped<Big16, LOAD_ROWS, LOAD_ROWS, false, MODE_WGRAD>(plan.grid, a, stream);
+  return launch_grouped<Small16, LOAD_ROWS, LOAD_ROWS, false, MODE_WGRAD>(plan.grid, a, stream);
+}
+
+#else
 
 // The launches of launch_tile, with the kernels' RAGGED flag R. Register
 // loading of both operands has no ragged variant (it bounds every element).
@@ -1224,29 +1560,31 @@ hipError_t G355_PART_LAUNCHER(G355_RAGGED, G355_PART)(const Plan& plan, const La
   return launch_tile_t<G355_RAGGED != 0>(plan, spec, args, stream);
 }
 
+#endif  // G355_I8 / G355_GROUPED / G355_WGRAD / dense
+
 #elif defined(G355_REDUCE)
 
-template <bool FP8, bool VEC>
+template <int TY, bool VEC>
 static hipError_t launch_reduce_k(const LaunchSpec& spec, const GemmArgs& a, hipStream_t stream) {
   const int64_t MN = static_cast<int64_t>(a.M) * a.N;
   const int64_t per_block = VEC ? 1024 : 256;
   const dim3 grid(static_cast<unsigned>((MN + per_block - 1) / per_block)), block(256);
   if (spec.out == OUT_BF16)
-    hipLaunchKernelGGL((VEC ? splitk_reduce4_kernel<FP8, OUT_BF16> : splitk_reduce_kernel<FP8, OUT_BF16>),
+    hipLaunchKernelGGL((VEC ? splitk_reduce4_kernel<TY, OUT_BF16> : splitk_reduce_kernel<TY, OUT_BF16>),
                        grid, block, 0, stream, a);
   else if (spec.out == OUT_I8)
-    hipLaunchKernelGGL((VEC ? splitk_reduce4_kernel<FP8, OUT_I8> : splitk_reduce_kernel<FP8, OUT_I8>),
+    hipLaunchKernelGGL((VEC ? splitk_reduce4_kernel<TY, OUT_I8> : splitk_reduce_kernel<TY, OUT_I8>),
                        grid, block, 0, stream, a);
   else if (spec.out == OUT_E4M3)
-    hipLaunchKernelGGL((VEC ? splitk_reduce4_kernel<FP8, OUT_E4M3> : splitk_reduce_kernel<FP8, OUT_E4M3>),
+    hipLaunchKernelGGL((VEC ? splitk_reduce4_kernel<TY, OUT_E4M3> : splitk_reduce_kernel<TY, OUT_E4M3>),
                        grid, block, 0, stream, a);
   else
-    hipLaunchKernelGGL((VEC ? splitk_reduce4_kernel<FP8, OUT_F32> : splitk_reduce_kernel<FP8, OUT_F32>),
+    hipLaunchKernelGGL((VEC ? splitk_reduce4_kernel<TY, OUT_F32> : splitk_reduce_kernel<TY, OUT_F32>),
                        grid, block, 0, stream, a);
   return hipGetLastError();
 }
 
-template <bool FP8>
+template <int TY>
 static hipError_t launch_reduce(const LaunchSpec& spec, const GemmArgs& a, hipStream_t stream) {
   const auto aligned16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
   // Four elements per thread only while that still gives 256 workgroups or
@@ -1254,8 +1592,8 @@ static hipError_t launch_reduce(const LaunchSpec& spec, const GemmArgs& a, hipSt
   const int64_t MN = static_cast<int64_t>(a.M) * a.N;
   const bool vec = MN >= 256 * 1024 && a.N % 4 == 0 && a.ldc % 4 == 0 &&
                    aligned16(a.workspace) && aligned16(a.C);
-  return vec ? launch_reduce_k<FP8, true>(spec, a, stream)
-             : launch_reduce_k<FP8, false>(spec, a, stream);
+  return vec ? launch_reduce_k<TY, true>(spec, a, stream)
+             : launch_reduce_k<TY, false>(spec, a, stream);
 }
 
 hipError_t launch_splitk_reduce(const Plan& plan, const LaunchSpec& spec, const GemmArgs& a,
@@ -1263,8 +1601,9 @@ hipError_t launch_splitk_reduce(const Plan& plan, const LaunchSpec& spec, const 
   (void)plan;
   // The FP32 per-row / per-column scales belong to plain FP8; MX scales were
   // applied inside the MFMAs.
-  return spec.fp8 && !spec.mx ? launch_reduce<true>(spec, a, stream)
-                              : launch_reduce<false>(spec, a, stream);
+  if (spec.i8) return launch_reduce<RED_I8>(spec, a, stream);
+  return spec.fp8 && !spec.mx ? launch_reduce<RED_FP8>(spec, a, stream)
+                              : launch_reduce<RED_PLAIN>(spec, a, stream);
 }
 
 #endif  // G355_PART / G355_REDUCE

@@ -15,6 +15,7 @@ enum Loader : int {
   LOAD_GENERIC = 1,  // any layout / alignment: element loads through registers
   LOAD_DIRECT_N = 2, // B only, BF16 N-contiguous (row-major), 16-byte aligned rows, N % 8 == 0:
                      // DMA into an N-major LDS tile, fragments by transposing LDS reads
+  LOAD_ROWS = 3,     // both operands of the weight gradient: as LOAD_DIRECT_N, any 2-byte alignment
 };
 
 enum KernelKind : int { KERNEL_TILE = 0, KERNEL_SKINNY = 1 };
@@ -32,6 +33,9 @@ struct Plan {
 // Chooses the kernel, tile and split for a shape (host arithmetic only).
 Plan make_plan(int64_t M, int64_t N, int64_t K, bool fp8);
 
+// Largest K of an INT8 product: K * 128 * 128 stays inside INT32.
+constexpr int64_t kMaxInt8K = 131071;
+
 // Largest K split a plan uses (the reduction kernel holds that many partials
 // per thread).
 constexpr int kMaxSplit = 16;
@@ -42,6 +46,7 @@ struct LaunchSpec {
   bool a_kmajor, b_kmajor; // layout of each operand (true = K contiguous)
   int out;                 // OutKind
   bool mx;                 // FP8 with E8M0 block scales (GemmArgs::mx_a / mx_b)
+  bool i8;                 // INT8 operands (fp8 false)
   bool ragged;             // K not a multiple of the 16-byte chunk, a K-major operand DMA-fed
 };
 
@@ -59,6 +64,34 @@ G355_DECLARE_PART(0, 0) G355_DECLARE_PART(0, 1) G355_DECLARE_PART(0, 2) G355_DEC
 G355_DECLARE_PART(0, 4) G355_DECLARE_PART(1, 0) G355_DECLARE_PART(1, 1) G355_DECLARE_PART(1, 2)
 G355_DECLARE_PART(1, 3) G355_DECLARE_PART(1, 4)
 #undef G355_DECLARE_PART
+
+// INT8 kernels, the same parts.
+#define G355_I8_LAUNCHER_(r, p) launch_i8_r##r##_p##p
+#define G355_I8_LAUNCHER(r, p) G355_I8_LAUNCHER_(r, p)
+#define G355_DECLARE_I8(r, p)                                                                \
+  hipError_t G355_I8_LAUNCHER(r, p)(const Plan& plan, const LaunchSpec& spec,                \
+                                    const GemmArgs& args, hipStream_t stream);
+G355_DECLARE_I8(0, 0) G355_DECLARE_I8(0, 1) G355_DECLARE_I8(0, 2) G355_DECLARE_I8(0, 3)
+G355_DECLARE_I8(0, 4) G355_DECLARE_I8(1, 0) G355_DECLARE_I8(1, 1) G355_DECLARE_I8(1, 2)
+G355_DECLARE_I8(1, 3) G355_DECLARE_I8(1, 4)
+#undef G355_DECLARE_I8
+
+// Products grouped by rows and their weight gradient: FP32 and BF16 output.
+struct GroupedPlan {
+  int bm, bn;    // tile
+  int64_t grid;  // workgroups
+};
+#define G355_GROUPED_LAUNCHER_(r, p) launch_grouped_r##r##_p##p
+#define G355_GROUPED_LAUNCHER(r, p) G355_GROUPED_LAUNCHER_(r, p)
+#define G355_WGRAD_LAUNCHER_(p) launch_wgrad_p##p
+#define G355_WGRAD_LAUNCHER(p) G355_WGRAD_LAUNCHER_(p)
+#define G355_DECLARE_GROUPED(name)                                                           \
+  hipError_t name(const GroupedPlan& plan, const LaunchSpec& spec, const GemmArgs& args,     \
+                  hipStream_t stream);
+G355_DECLARE_GROUPED(G355_GROUPED_LAUNCHER(0, 1)) G355_DECLARE_GROUPED(G355_GROUPED_LAUNCHER(0, 2))
+G355_DECLARE_GROUPED(G355_GROUPED_LAUNCHER(1, 1)) G355_DECLARE_GROUPED(G355_GROUPED_LAUNCHER(1, 2))
+G355_DECLARE_GROUPED(G355_WGRAD_LAUNCHER(1)) G355_DECLARE_GROUPED(G355_WGRAD_LAUNCHER(2))
+#undef G355_DECLARE_GROUPED
 
 // Enqueue the tile kernel of a plan (the part launcher for its output kind
 // and ragged flag). Returns the HIP error of the launch.
@@ -80,6 +113,12 @@ hipError_t launch_splitk_reduce(const Plan& plan, const LaunchSpec& spec, const 
 // rows with K and ldx multiples of 8 and Q rows 8-byte aligned.
 hipError_t launch_quantize_rows(int64_t M, int64_t K, const void* X, int64_t ldx, void* Q,
                                 int64_t ldq, float* scale, bool vec, hipStream_t stream);
+
+// The same for INT8 codes, and the row sums of an INT8 weight (quant.hip).
+hipError_t launch_quantize_int8_rows(int64_t M, int64_t K, const void* X, int64_t ldx, void* Q,
+                                     int64_t ldq, float* scale, bool vec, hipStream_t stream);
+hipError_t launch_int8_row_sums(int64_t N, int64_t K, const void* B, int64_t ldb, int32_t* sums,
+                                hipStream_t stream);
 
 // One-time reorder of B (K x N, elements of elem_bytes) into K-major rows of
 // ldbp elements (pack.hip). b_rowmajor: B is N-contiguous (b(k,n) = B[k*ldb+n]).

@@ -243,6 +243,139 @@ gemm_status gemm_quantize_fp8_rows(int64_t M, int64_t K, const void* X, int64_t 
                                    void* Q, int64_t ldq, float* scale, void* stream);
 
 /*
+ * INT8 x INT8 product with one FP32 scale per row of A (token) and per column
+ * of B (channel), and an optional zero point per row of A:
+ *
+ *   C = act( alpha * (scale_a[m] * scale_b[n]) * S(m,n) + beta * C + bias[n] )
+ *   S(m,n) = sum_k (a(m,k) - zero_a[m]) b(k,n) = sum_k a b - zero_a[m] * sum_b[n]
+ *
+ * The sum over k is an exact INT32 sum whatever the split of K, and
+ * zero_a[m] * sum_b[n] is taken off exactly before the first rounding; the
+ * epilogue is FP32, as in the other calls. It reads what gemm_*_quant with
+ * GEMM_QOUT_INT8 writes: scale_a[m] = 1 / out_scale[m], zero_a = out_zero.
+ * A: INT8, ROW (K-major), lda >= K. B: INT8, COL (K-major), ldb >= K; other
+ * layouts return GEMM_ERR_UNSUPPORTED (gemm_pack_b with elem_bytes 1 reorders
+ * a weight). Any byte alignment. K at most 131071 (the INT32 sum cannot
+ * overflow), else GEMM_ERR_UNSUPPORTED.
+ * scale_a FP32[M], scale_b FP32[N]: required. zero_a: INT32[M] of magnitude
+ * below 2^24; sum_b: INT32[N], sum_b[n] = sum_k b(k,n) (gemm_int8_col_sums);
+ * both NULL for symmetric codes, one alone returns GEMM_ERR_NULL_POINTER.
+ * workspace: at least gemm_workspace_size(M, N, K, 1) bytes.
+ */
+gemm_status gemm_int8_scaled(int64_t M, int64_t N, int64_t K, float alpha,
+                             const void* A, int64_t lda, gemm_layout layout_a,
+                             const void* B, int64_t ldb, gemm_layout layout_b,
+                             const float* scale_a, const int32_t* zero_a,
+                             const float* scale_b, const int32_t* sum_b,
+                             float beta, void* C, int64_t ldc, gemm_out_dtype c_dtype,
+                             const void* bias, gemm_act act,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* gemm_int8_scaled with the quantising epilogue of gemm_bf16_quant. */
+gemm_status gemm_int8_scaled_quant(int64_t M, int64_t N, int64_t K, float alpha,
+                                   const void* A, int64_t lda, gemm_layout layout_a,
+                                   const void* B, int64_t ldb, gemm_layout layout_b,
+                                   const float* scale_a, const int32_t* zero_a,
+                                   const float* scale_b, const int32_t* sum_b,
+                                   const void* bias, gemm_act act,
+                                   const float* out_scale, const int32_t* out_zero,
+                                   void* Q, int64_t ldq, gemm_qout_dtype q_dtype,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Per-token INT8 quantisation of BF16 activations, the A operand and scale_a
+ * of gemm_int8_scaled. For each row m of X:
+ *   scale[m]   = fp32(max_k |x(m,k)| / 127), or 1 if the row is all zero
+ *   Q[m*ldq+k] = round-to-nearest-even of fp32(x(m,k) / scale[m]), in [-127, 127]
+ * Arguments, edge cases and errors as for gemm_quantize_fp8_rows. A row with a
+ * NaN or an infinity gets undefined codes and scale; other rows are untouched
+ * by it.
+ */
+gemm_status gemm_quantize_int8_rows(int64_t M, int64_t K, const void* X, int64_t ldx,
+                                    void* Q, int64_t ldq, float* scale, void* stream);
+
+/*
+ * sums[n] = sum_k b(k,n) of an INT8 weight in COL layout (N rows of ldb >= K
+ * bytes), the sum_b of the INT8 products. Once per weight. K at most 131071.
+ * Errors: GEMM_ERR_BAD_DIM, GEMM_ERR_UNSUPPORTED (K), GEMM_ERR_BAD_LD,
+ * GEMM_ERR_NULL_POINTER, GEMM_ERR_HIP. K == 0 writes zeros.
+ */
+gemm_status gemm_int8_col_sums(int64_t K, int64_t N, const void* B, int64_t ldb,
+                               int32_t* sums, void* stream);
+
+/*
+ * Products grouped by rows: the rows of A belong to G groups ("experts"), each
+ * with a weight of its own. Rows offsets[g] .. offsets[g+1]-1 of A and C are
+ * group g's:
+ *
+ *   C[r,n] = act( alpha * (scale_a[r] * scale_b[g][n]) * sum_k A[r,k] B_g[k,n]
+ *                 + beta * C[r,n] + bias[g][n] )          (scales: 8-bit calls)
+ *
+ * T rows in all. A: T x K, ROW layout (tokens sorted by group), lda >= K.
+ * offsets: DEVICE INT32[G+1], 4-byte aligned, non-decreasing, within [0, T];
+ * no host copy is needed and nothing is synchronised. Groups may be empty and
+ * of any length. Rows before offsets[0] or from offsets[G] on belong to no
+ * group: their rows of C are neither read nor written, so A and C may be
+ * buffers of a fixed capacity T. Offsets that decrease or leave [0, T] give
+ * undefined results in C, but no access outside the arrays.
+ * B: group g's weight starts stride_b elements after group g-1's (stride_b >=
+ * 0; 0 shares one weight); layout_b and ldb describe each as in gemm_bf16.
+ * gemm_grouped_bf16 takes both layouts: with weights stored as N rows of K
+ * (COL) the call is the layer's forward pass, and the same array read as
+ * ROW, K and N exchanged, is its input gradient dX = dY W. The 8-bit calls
+ * take COL only (GEMM_ERR_UNSUPPORTED). bias: BF16[G][N] or NULL; scale_a:
+ * FP32[T]; scale_b: FP32[G][N]; zero_a INT32[T] and sum_b INT32[G][N] as in
+ * gemm_int8_scaled. C: T x N, ldc >= N. No workspace.
+ * G == 0, T == 0 or N == 0 launches nothing; K == 0 as in gemm_bf16.
+ * Errors: GEMM_ERR_BAD_ENUM, GEMM_ERR_BAD_DIM (a size negative or above 2^30,
+ * G above 65536), GEMM_ERR_BAD_LD (a leading dimension, or stride_b < 0),
+ * GEMM_ERR_NULL_POINTER, GEMM_ERR_UNSUPPORTED (layout, INT8 K above 131071,
+ * offsets not 4-byte aligned), GEMM_ERR_HIP; before anything is enqueued
+ * except the last.
+ */
+gemm_status gemm_grouped_bf16(int64_t G, int64_t T, int64_t N, int64_t K, float alpha,
+                              const void* A, int64_t lda, const int32_t* offsets,
+                              const void* B, int64_t ldb, gemm_layout layout_b, int64_t stride_b,
+                              float beta, void* C, int64_t ldc, gemm_out_dtype c_dtype,
+                              const void* bias, gemm_act act, void* stream);
+
+gemm_status gemm_grouped_fp8_scaled(int64_t G, int64_t T, int64_t N, int64_t K, float alpha,
+                                    const void* A, int64_t lda, const int32_t* offsets,
+                                    const void* B, int64_t ldb, gemm_layout layout_b,
+                                    int64_t stride_b, const float* scale_a, const float* scale_b,
+                                    float beta, void* C, int64_t ldc, gemm_out_dtype c_dtype,
+                                    const void* bias, gemm_act act, void* stream);
+
+gemm_status gemm_grouped_int8_scaled(int64_t G, int64_t T, int64_t N, int64_t K, float alpha,
+                                     const void* A, int64_t lda, const int32_t* offsets,
+                                     const void* B, int64_t ldb, gemm_layout layout_b,
+                                     int64_t stride_b, const float* scale_a,
+                                     const int32_t* zero_a, const float* scale_b,
+                                     const int32_t* sum_b, float beta, void* C, int64_t ldc,
+                                     gemm_out_dtype c_dtype, const void* bias, gemm_act act,
+                                     void* stream);
+
+/*
+ * Weight gradient of gemm_grouped_bf16: for every group g,
+ *
+ *   C_g[n,k] = alpha * sum over g's rows r of D[r,n] X[r,k] + beta * C_g[n,k]
+ *
+ * D: BF16, T x N (the gradient of the output), ldd >= N. X: BF16, T x K (the
+ * layer's input), ldx >= K. offsets as above; an empty group's gradient is
+ * beta * C_g (zeros for beta == 0, C then not being read). C_g: N rows of
+ * ldc >= K, c_dtype FP32 or BF16, the layout of a COL weight (exchange D and
+ * X for a ROW one); group g's starts stride_c elements after group g-1's,
+ * stride_c >= (N-1)*ldc + K where G > 1 (else GEMM_ERR_BAD_LD). beta = 1 adds
+ * to the gradient of earlier micro-batches. Sums are FP32. No workspace.
+ * G == 0, N == 0 or K == 0 launches nothing; T == 0 leaves beta * C.
+ * Other errors as above.
+ */
+gemm_status gemm_grouped_bf16_wgrad(int64_t G, int64_t T, int64_t N, int64_t K, float alpha,
+                                    const void* D, int64_t ldd, const void* X, int64_t ldx,
+                                    const int32_t* offsets, float beta, void* C, int64_t ldc,
+                                    int64_t stride_c, gemm_out_dtype c_dtype, void* stream);
+
+/*
  * One-time reorder of a weight matrix B (logical K x N) into the layout the
  * fast path reads: Bp[n*ldbp + k] = b(k, n), i.e. GEMM_COL_MAJOR (K-major)
  * with leading dimension ldbp. The FP8 DeepGEMM page (sec. 3.2) rearranges B
@@ -271,7 +404,7 @@ gemm_status gemm_pack_b(int64_t K, int64_t N, const void* B, int64_t ldb, gemm_l
  * kernel needs none). Pure host arithmetic; callable without a GPU. Query
  * once and allocate up front (the FP8 page's interface, sec. 5.1, separates
  * the size query from the call for the same reason). is_fp8: 0 for
- * gemm_bf16, 1 for gemm_fp8_scaled. Negative sizes return 0.
+ * gemm_bf16, 1 for gemm_fp8_scaled and gemm_int8_scaled. Negative sizes return 0.
  */
 size_t gemm_workspace_size(int64_t M, int64_t N, int64_t K, int is_fp8);
 
