@@ -32,6 +32,7 @@ SOURCES += [("gemm_tile.hip", f"gemm_grouped_r{r}_p{p}",
             for r in (0, 1) for p in (1, 2)]
 SOURCES += [("gemm_tile.hip", f"gemm_wgrad_p{p}",
              ["-DG355_WGRAD=1", "-DG355_RAGGED=0", f"-DG355_PART={p}"]) for p in (1, 2)]
+SOURCES += [("gemm_turn.hip", f"gemm_turn_{f}", [f"-DG355_TURN={f}"]) for f in range(4)]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -38,13 +38,10 @@
 #include <type_traits>
 
 #include "common.hpp"
+#include "grouping.hpp"
 #include "internal.hpp"
 
 namespace g355 {
-
-// Word 3 of a raw buffer descriptor on gfx9-family parts (32-bit data format,
-// no swizzle, no index stride).
-constexpr int kBufferWord3 = 0x00020000;
 
 // Physical chunk offset of row r for CPR chunks per row (see file comment).
 template <int CPR>
@@ -667,68 +664,6 @@ __device__ __forceinline__ void run_epilogue(const GemmArgs& p,
   }
 }
 
-// ------------------------------------------------------- products grouped by rows
-
-// MODE_GROUPED: rows offsets[g] .. offsets[g+1]-1 of A and C belong to group
-// g, which has a B (bias, scale_b, sum_b) of its own. MODE_WGRAD: C of group g
-// is the product of two operands over those rows (their contraction axis).
-enum TileMode : int { MODE_DENSE = 0, MODE_GROUPED = 1, MODE_WGRAD = 2 };
-
-// Group g's rows [s, e). The offsets are device data that no host check has
-// seen: clamped here, so that whatever they hold no access leaves the arrays.
-__device__ __forceinline__ void group_rows(const GemmArgs& p, int g, int& s, int& e) {
-  s = min(max(p.offsets[g], 0), p.rows_total);
-  e = min(max(p.offsets[g + 1], s), p.rows_total);
-}
-
-// The row tile of workgroup `b`: every wave counts the row tiles of all groups
-// (64 groups at a time, one per lane) and finds its own in their running sum,
-// so the launch needs neither a host copy of the offsets nor a kernel before
-// it. The grid is the largest count possible; workgroups past the real one
-// (nwg) return, and the real ones are spread over the XCDs evenly.
-// tiles: row tiles of the found group; first: row tiles of the groups before it.
-template <int BM>
-__device__ __forceinline__ bool find_group(const GemmArgs& p, int b, int lane, int& L, int& g,
-                                           int& s, int& rows, int& tiles, int& first) {
-  const auto count = [&](int c, int& gs, int& ge) {
-    gs = ge = 0;
-    if (c + lane < p.groups) group_rows(p, c + lane, gs, ge);
-    return (ge - gs + BM - 1) / BM;
-  };
-  const auto running_sum = [&](int n) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int t = __shfl_up(n, o);
-      n += lane >= o ? t : 0;
-    }
-    return n;
-  };
-  int gs, ge, total = 0;
-  for (int c = 0; c < p.groups; c += 64) total += __shfl(running_sum(count(c, gs, ge)), 63);
-  total = __builtin_amdgcn_readfirstlane(total);
-  const int nwg = total * p.tiles_n;
-  if (b >= nwg) return false;
-  L = xcd_remap(b, nwg);
-  const int rt = L / p.tiles_n;
-  int before = 0;
-  for (int c = 0; c < p.groups; c += 64) {
-    const int n = count(c, gs, ge);
-    const int incl = running_sum(n);
-    const unsigned long long hit = __ballot(before + incl > rt);
-    if (hit != 0) {
-      const int src = __builtin_ctzll(hit);
-      g = c + src;
-      s = __builtin_amdgcn_readlane(gs, src);
-      rows = __builtin_amdgcn_readlane(ge, src) - s;
-      tiles = __builtin_amdgcn_readlane(n, src);
-      first = before + __builtin_amdgcn_readlane(incl, src) - tiles;
-      return true;
-    }
-    before += __builtin_amdgcn_readlane(incl, 63);
-  }
-  return false;  // not reached: rt < total
-}
-
 // ------------------------------------------------------------------- the kernel
 
 // RAGGED: K may end inside a 16-byte chunk of a DMA-fed row (patch_tail).
@@ -758,7 +693,7 @@ gemm_tile_kernel(GemmArgs p) {
   } else if constexpr (MODE == MODE_GROUPED) {
     int L, g, s, rows, tiles, first;
     if (!find_group<C::BM>(p, blockIdx.x, lane, L, g, s, rows, tiles, first)) return;
-    tile_coords(L - first * p.tiles_n, tiles, p.tiles_n, 4, tm, tn);
+    tile_coords(L - first * p.tiles_n, tiles, p.tiles_n, kGroupedBand, tm, tn);
     // The operands of this row tile alone, its first row as row 0: 64-bit
     // pointer arithmetic here, so that the kernel's 32-bit offsets never see
     // more than a tile's rows or one group's weight.
@@ -779,19 +714,8 @@ gemm_tile_kernel(GemmArgs p) {
       }
     }
   } else {
-    // Every group has the same tiles; the groups differ in their K range. Each
-    // XCD takes an eighth of every group's tiles, neighbours of each other, so
-    // that groups of unequal length load the XCDs alike.
-    const int tiles = p.tiles_m * p.tiles_n;
-    const int b = blockIdx.x;
-    int g = b / tiles, t = b - g * tiles;
-    if (tiles >= kWgradXcdTiles) {
-      const int per = (tiles + 7) / 8;
-      g = (b >> 3) / per;
-      t = (b & 7) * per + (b >> 3) - g * per;
-      if (t >= tiles) return;
-    }
-    tile_coords(t, p.tiles_m, p.tiles_n, 4, tm, tn);
+    int g;
+    if (!wgrad_tile(p, blockIdx.x, g, tm, tn)) return;
     int s, e;
     group_rows(p, g, s, e);
     p.K = __builtin_amdgcn_readfirstlane(e - s);
@@ -1448,12 +1372,11 @@ hipError_t G355_I8_LAUNCHER(G355_RAGGED, G355_PART)(const Plan& plan, const Laun
 
 #elif defined(G355_GROUPED)
 
-// One element type's tiles: 256x256, 128x128, and 64x128 with a deep ring.
-template <class BIG, class SMALL, class NARROW, int LB>
+// One element type's tiles: 128x128, and 64x128 with a deep ring.
+template <class SMALL, class NARROW, int LB>
 static hipError_t launch_grouped_type(const GroupedPlan& plan, const GemmArgs& a,
                                       hipStream_t stream) {
   constexpr bool R = G355_RAGGED != 0;
-  if (plan.bm == 256) return launch_grouped<BIG, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
   if (plan.bm == 64) return launch_grouped<NARROW, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
   return launch_grouped<SMALL, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
 }
@@ -1471,11 +1394,11 @@ hipError_t G355_GROUPED_LAUNCHER(G355_RAGGED, G355_PART)(const GroupedPlan& plan
     else
       return launch_grouped<Small16, LOAD_GENERIC, LOAD_GENERIC, false, MODE_GROUPED>(plan.grid, a, stream);
   }
-  if (spec.i8) return launch_grouped_type<BigI8, SmallI8, NarrowI8, LOAD_DIRECT>(plan, a, stream);
-  if (spec.fp8) return launch_grouped_type<Big8, Small8, Narrow8, LOAD_DIRECT>(plan, a, stream);
+  if (spec.i8) return launch_grouped_type<SmallI8, NarrowI8, LOAD_DIRECT>(plan, a, stream);
+  if (spec.fp8) return launch_grouped_type<Small8, Narrow8, LOAD_DIRECT>(plan, a, stream);
   if (spec.loader_b == LOAD_DIRECT_N)
-    return launch_grouped_type<Big16, Small16, Narrow16, LOAD_DIRECT_N>(plan, a, stream);
-  return launch_grouped_type<Big16, Small16, Narrow16, LOAD_DIRECT>(plan, a, stream);
+    return launch_grouped_type<Small16, Narrow16, LOAD_DIRECT_N>(plan, a, stream);
+  return launch_grouped_type<Small16, Narrow16, LOAD_DIRECT>(plan, a, stream);
 }
 
 #elif defined(G355_WGRAD)
@@ -1484,8 +1407,6 @@ hipError_t G355_WGRAD_LAUNCHER(G355_PART)(const GroupedPlan& plan, const LaunchS
                                           const GemmArgs& a, hipStream_t stream) {
   if (spec.loader_a == LOAD_GENERIC)
     return launch_grouped<Small16, LOAD_GENERIC, LOAD_GENERIC, false, MODE_WGRAD>(plan.grid, a, stream);
-  if (plan.bm == 256)
-    return launch_grouped<Big16, LOAD_ROWS, LOAD_ROWS, false, MODE_WGRAD>(plan.grid, a, stream);
   return launch_grouped<Small16, LOAD_ROWS, LOAD_ROWS, false, MODE_WGRAD>(plan.grid, a, stream);
 }
 

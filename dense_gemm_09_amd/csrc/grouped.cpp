@@ -118,7 +118,7 @@ gemm_status run_grouped(ElemType type, int64_t G, int64_t T, int64_t N, int64_t 
   LaunchSpec spec{};
   spec.fp8 = type == TY_FP8;
   spec.i8 = type == TY_I8;
-  spec.out = c_dtype;
+  spec.out = c_dtype == GEMM_OUT_F32 ? OUT_F32 : OUT_BF16;
   spec.a_kmajor = true;
   spec.b_kmajor = b_kmajor;
   // DMA: 32-bit offsets into a tile's rows of A and into one group's weight.
@@ -166,7 +166,11 @@ gemm_status run_grouped(ElemType type, int64_t G, int64_t T, int64_t N, int64_t 
   (void)hipGetLastError();  // an earlier call's pending error is not this call's
   const auto s = static_cast<hipStream_t>(stream);
   hipError_t err;
-  if (c_dtype == GEMM_OUT_F32)
+  if (plan.bm == 256)
+    err = spec.i8    ? launch_turn_i8(spec, plan.grid, a, s)
+          : spec.fp8 ? launch_turn_fp8(spec, plan.grid, a, s)
+                     : launch_turn_bf16(spec, plan.grid, a, s);
+  else if (c_dtype == GEMM_OUT_F32)
     err = spec.ragged ? launch_grouped_r1_p1(plan, spec, a, s) : launch_grouped_r0_p1(plan, spec, a, s);
   else
     err = spec.ragged ? launch_grouped_r1_p2(plan, spec, a, s) : launch_grouped_r0_p2(plan, spec, a, s);
@@ -228,7 +232,7 @@ gemm_status gemm_grouped_bf16_wgrad(int64_t G, int64_t T, int64_t N, int64_t K, 
 
   GroupedPlan plan = plan_wgrad(G, N, K);
   LaunchSpec spec{};
-  spec.out = c_dtype;
+  spec.out = c_dtype == GEMM_OUT_F32 ? OUT_F32 : OUT_BF16;
   // DMA: 32-bit offsets into the 64 rows of a slice.
   const bool dma = T == 0 || (128 * std::max(ldd, ldx) < k2G &&
                               rows_dma_ok(D, ldd, 0, (T - 1) * ldd + N - 1) &&
@@ -262,8 +266,9 @@ gemm_status gemm_grouped_bf16_wgrad(int64_t G, int64_t T, int64_t N, int64_t K, 
   a.stride_b = stride_c;
   (void)hipGetLastError();
   const auto s = static_cast<hipStream_t>(stream);
-  const hipError_t err = c_dtype == GEMM_OUT_F32 ? launch_wgrad_p1(plan, spec, a, s)
-                                                 : launch_wgrad_p2(plan, spec, a, s);
+  const hipError_t err = plan.bm == 256             ? launch_turn_wgrad(spec, plan.grid, a, s)
+                         : c_dtype == GEMM_OUT_F32 ? launch_wgrad_p1(plan, spec, a, s)
+                                                   : launch_wgrad_p2(plan, spec, a, s);
   return err == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }
 

@@ -93,6 +93,14 @@ G355_DECLARE_GROUPED(G355_GROUPED_LAUNCHER(1, 1)) G355_DECLARE_GROUPED(G355_GROU
 G355_DECLARE_GROUPED(G355_WGRAD_LAUNCHER(1)) G355_DECLARE_GROUPED(G355_WGRAD_LAUNCHER(2))
 #undef G355_DECLARE_GROUPED
 
+// 256x256 tiles with FP32 or BF16 output (gemm_turn.hip), one element type
+// each: grouped products (INT8: the dense one too, where groups is 0) and the
+// weight gradient.
+hipError_t launch_turn_bf16(const LaunchSpec& spec, int64_t grid, const GemmArgs& args, hipStream_t stream);
+hipError_t launch_turn_fp8(const LaunchSpec& spec, int64_t grid, const GemmArgs& args, hipStream_t stream);
+hipError_t launch_turn_i8(const LaunchSpec& spec, int64_t grid, const GemmArgs& args, hipStream_t stream);
+hipError_t launch_turn_wgrad(const LaunchSpec& spec, int64_t grid, const GemmArgs& args, hipStream_t stream);
+
 // Enqueue the tile kernel of a plan (the part launcher for its output kind
 // and ragged flag). Returns the HIP error of the launch.
 hipError_t launch_tile(const Plan& plan, const LaunchSpec& spec, const GemmArgs& args,
