@@ -57,8 +57,12 @@ struct GemmArgs {
   const int32_t* offsets; // INT32[groups + 1]: group g has rows offsets[g] .. offsets[g+1]-1
   int groups;
   int rows_total;         // rows of A and C (weight gradient: of A and B)
+  int turn_tiles;         // tiles of a launch of gemm_turn.hip (grouped: at most)
   int64_t stride_b;       // elements from one group's B (weight gradient: C) to the next
 };
+
+// Groups that gemm_turn.hip's table of them holds (a multiple of 64).
+constexpr int kTableGroups = 1024;
 
 // Tiles per group from which the weight gradient deals each group's tiles to
 // the XCDs in eighths (below, workgroups go round robin: an eighth of fewer

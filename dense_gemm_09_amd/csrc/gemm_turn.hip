@@ -40,13 +40,13 @@
 namespace g355 {
 
 constexpr int kTurnThreads = 512;
+constexpr int64_t kTurnGrid = 256;  // a workgroup on every CU
 constexpr int kBuf = 32768;     // one operand's slice
 constexpr int kHalf = 16384;    // half of its rows (or columns)
 constexpr int kBBase = 65536;   // B's two slices follow A's
 constexpr int kAhead = 10;      // copies of later turns that may be in flight
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 // Global vectors at any element alignment (the hardware takes them).
 typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
@@ -88,19 +88,20 @@ __device__ __forceinline__ int rows_swizzle(int k) {
 // ------------------------------------------------------------------------ copies
 
 // K-major operand: each wave copies 16 rows of a half in two instructions of
-// eight rows of 128 bytes. Rows past the operand's end repeat its last row
-// (their results are never stored); chunks that do not end by k_end read zeros:
-// they get an offset past the descriptor's range.
+// eight rows of 128 bytes. Rows past the tile's `rows` repeat its last one
+// (their results are never stored); chunks that do not end by K read zeros:
+// they get an offset past the descriptor's range. Offsets are from the tile's
+// first row, 32 bits (the host checks 256 rows).
 template <class C, bool PAIRED>
 struct KMajorCopy {
   uint32_t off[2][2];
   int last[2];  // K element after the lane's chunk, slice-relative
   __amdgpu_buffer_rsrc_t rsrc;
   uint32_t extent;
-  __device__ __forceinline__ void init(const void* ptr, int64_t ld, int row0, int rows, int K,
-                                       int wave, int lane) {
-    extent = static_cast<uint32_t>((static_cast<int64_t>(rows - 1) * ld + K) * C::ES);
-    rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(ptr), 0, static_cast<int>(extent),
+  __device__ __forceinline__ void next() {}
+  __device__ __forceinline__ void point(const char* ptr, int64_t ld, int rows, int K, int wave, int lane) {
+    extent = static_cast<uint32_t>((static_cast<uint32_t>(rows - 1) * static_cast<uint32_t>(ld) + K) * C::ES);
+    rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(ptr), 0, static_cast<int>(extent),
                                              kBufferWord3);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -108,16 +109,14 @@ struct KMajorCopy {
       const int c = (lane & 7) ^ turn_swizzle<PAIRED>(r);
       last[q] = c * C::CE + C::CE;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int g = min(row0 + 128 * h + r, rows - 1);
-        off[h][q] = static_cast<uint32_t>(static_cast<int64_t>(g) * ld * C::ES) + c * 16;
-      }
+      for (int h = 0; h < 2; ++h)
+        off[h][q] = static_cast<uint32_t>(min(128 * h + r, rows - 1)) * static_cast<uint32_t>(ld * C::ES) + c * 16;
     }
   }
-  __device__ __forceinline__ void issue(char* half, int h, int wave, int k0, int k_end) const {
+  __device__ __forceinline__ void issue(char* half, int h, int wave, int k0, int K) const {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const uint32_t vo = k0 + last[q] <= k_end ? off[h][q] : extent;
+      const uint32_t vo = k0 + last[q] <= K ? off[h][q] : extent;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (G355_LDS void*)(half + (2 * wave + q) * 1024),
                                                16, static_cast<int>(vo), k0 * C::ES, 0, 0);
     }
@@ -126,40 +125,40 @@ struct KMajorCopy {
 
 // Operand whose rows run along K (BF16): a half is 128 of its columns, each
 // wave copies eight rows of them. The descriptor's base moves with the slice,
-// so that any number of rows can be addressed, and its range ends with row
-// k_end - 1, so that later rows read zeros. A chunk that straddles the last
-// column brings in what follows the row, for columns that are never stored. The
-// range check drops a 4-byte word that lies partly past the range, which for an
-// odd column count holds the last element: the range is 2 bytes longer (the
-// host makes sure that those stay on the operand's last page).
+// so that any number of rows can be addressed, and in the last slice its range
+// ends with row K - 1, so that later rows read zeros. A chunk that straddles the last of the
+// tile's `cols` brings in what follows the row, for columns that are never
+// stored. The range check drops a 4-byte word that lies partly past the range,
+// which for an odd column count holds the last element: the range is 2 bytes
+// longer (the host makes sure that those stay on the operand's last page).
 template <class C, bool PAIRED>
 struct RowsCopy {
   uint32_t off[2][2];
-  const char* base;
-  int64_t ld2;  // bytes per row
-  int cols;
-  __device__ __forceinline__ void init(const void* ptr, int64_t ld, int col0, int cols_, int,
-                                       int wave, int lane) {
-    base = static_cast<const char*>(ptr);
-    ld2 = ld * 2;
-    cols = cols_;
+  const char* base;  // of the slice
+  int64_t step;      // bytes per slice
+  int ld2, last;     // bytes per row, and of the last row (with the 2 more)
+  __device__ __forceinline__ void next() { base += step; }
+  __device__ __forceinline__ void point(const char* ptr, int64_t ld, int cols, int, int wave, int lane) {
+    base = ptr;
+    step = ld * 2 * C::BKE;
+    ld2 = static_cast<int>(ld * 2);
+    last = cols * 2 + 2;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int k = 8 * wave + 4 * q + (lane >> 4);
       const int c = (lane & 15) ^ rows_swizzle<PAIRED>(k);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int n = col0 + 128 * h + 8 * c;
-        off[h][q] = n < cols ? static_cast<uint32_t>(k * ld2 + n * 2) : 0x80000000u;
+        const int n = 128 * h + 8 * c;
+        off[h][q] = n < cols ? static_cast<uint32_t>(k * ld2) + n * 2 : 0x80000000u;
       }
     }
   }
-  __device__ __forceinline__ void issue(char* half, int h, int wave, int k0, int k_end) const {
-    const int rem = k_end - k0;
-    const int64_t want = rem > 0 ? (rem - 1) * ld2 + cols * 2 + 2 : 0;
-    const int range = static_cast<int>(want < INT32_MAX ? want : INT32_MAX);
-    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(base + k0 * ld2), 0, range, kBufferWord3);
+  __device__ __forceinline__ void issue(char* half, int h, int wave, int k0, int K) const {
+    const int rem = K - k0;
+    const int range = rem >= C::BKE ? INT32_MAX : rem > 0 ? (rem - 1) * ld2 + last : 0;
+    const __amdgpu_buffer_rsrc_t rsrc =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, range, kBufferWord3);
 #pragma unroll
     for (int q = 0; q < 2; ++q)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (G355_LDS void*)(half + (2 * wave + q) * 1024),
@@ -169,6 +168,9 @@ struct RowsCopy {
 
 // --------------------------------------------------------------------- fragments
 
+// Both pieces of a block's fragment.
+__device__ __forceinline__ i32x4 low(const i32x8& x) { return __builtin_shufflevector(x, x, 0, 1, 2, 3); }
+__device__ __forceinline__ i32x4 high(const i32x8& x) { return __builtin_shufflevector(x, x, 4, 5, 6, 7); }
 // Fragments of one operand: NB blocks of 16 rows (columns of C) per half, two
 // 16-byte pieces each (64 bytes of K a piece over the four lane groups).
 template <class C, int NB, bool ROWS, bool PAIRED>
@@ -199,149 +201,199 @@ struct Fragments {
     }
   }
 
-  // Piece t of block b in the half that starts `at` bytes into the operand's LDS.
-  __device__ __forceinline__ i32x4 read(const char* smem, int at, int b, int t) const {
+  // All blocks of the half that starts AT bytes into the operand's LDS.
+  template <int AT>
+  __device__ __forceinline__ void read(i32x8 (&f)[NB]) const {
+    // Written out, with the wait for them: before its own reads of LDS the
+    // compiler waits for every copy in flight.
     if constexpr (!ROWS) {
-      return *reinterpret_cast<const i32x4*>(smem + addr[t] + at + b * (PAIRED ? 4 : 16) * 128);
+      i32x4 v[NB][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          v[b][t] = *reinterpret_cast<G355_LDS const i32x4*>(addr[t] + AT + b * (PAIRED ? 4 : 16) * 128);
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        f[b] = __builtin_shufflevector(v[b][0], v[b][1], 0, 1, 2, 3, 4, 5, 6, 7);
     } else {
-      const char* q = smem + addr[PAIRED ? 0 : b] + at + t * 32 * 256 + (PAIRED ? 8 * b : 0);
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((G355_LDS s16x4*)q);
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((G355_LDS s16x4*)(q + 4 * 256));
-      return __builtin_bit_cast(i32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      i32x2 v[NB][4];
+      constexpr int P = PAIRED ? 8 : 0;  // bytes from one block to the next
+      if constexpr (NB == 2) {
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %8 offset:%10\n\tds_read_b64_tr_b16 %1, %8 offset:%11\n\t"
+            "ds_read_b64_tr_b16 %4, %9 offset:%14\n\tds_read_b64_tr_b16 %5, %9 offset:%15\n\t"
+            "ds_read_b64_tr_b16 %2, %8 offset:%12\n\tds_read_b64_tr_b16 %3, %8 offset:%13\n\t"
+            "ds_read_b64_tr_b16 %6, %9 offset:%16\n\tds_read_b64_tr_b16 %7, %9 offset:%17\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[0][2]), "=&v"(v[0][3]), "=&v"(v[1][0]),
+              "=&v"(v[1][1]), "=&v"(v[1][2]), "=&v"(v[1][3])
+            : "v"(addr[0]), "v"(addr[NA - 1]), "n"(AT), "n"(AT + 1024), "n"(AT + 8192), "n"(AT + 9216),
+              "n"(AT + P), "n"(AT + P + 1024), "n"(AT + P + 8192), "n"(AT + P + 9216)
+            : "memory");
+      } else {
+        static_assert(NB == 4 && !PAIRED, "A's blocks");
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %16 offset:%20\n\tds_read_b64_tr_b16 %1, %16 offset:%21\n\t"
+            "ds_read_b64_tr_b16 %4, %17 offset:%20\n\tds_read_b64_tr_b16 %5, %17 offset:%21\n\t"
+            "ds_read_b64_tr_b16 %8, %18 offset:%20\n\tds_read_b64_tr_b16 %9, %18 offset:%21\n\t"
+            "ds_read_b64_tr_b16 %12, %19 offset:%20\n\tds_read_b64_tr_b16 %13, %19 offset:%21\n\t"
+            "ds_read_b64_tr_b16 %2, %16 offset:%22\n\tds_read_b64_tr_b16 %3, %16 offset:%23\n\t"
+            "ds_read_b64_tr_b16 %6, %17 offset:%22\n\tds_read_b64_tr_b16 %7, %17 offset:%23\n\t"
+            "ds_read_b64_tr_b16 %10, %18 offset:%22\n\tds_read_b64_tr_b16 %11, %18 offset:%23\n\t"
+            "ds_read_b64_tr_b16 %14, %19 offset:%22\n\tds_read_b64_tr_b16 %15, %19 offset:%23\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[0][2]), "=&v"(v[0][3]), "=&v"(v[1][0]),
+              "=&v"(v[1][1]), "=&v"(v[1][2]), "=&v"(v[1][3]), "=&v"(v[2][0]), "=&v"(v[2][1]),
+              "=&v"(v[2][2]), "=&v"(v[2][3]), "=&v"(v[3][0]), "=&v"(v[3][1]), "=&v"(v[3][2]),
+              "=&v"(v[3][3])
+            : "v"(addr[0]), "v"(addr[1]), "v"(addr[2]), "v"(addr[NA - 1]), "n"(AT), "n"(AT + 1024),
+              "n"(AT + 8192), "n"(AT + 9216)
+            : "memory");
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        f[b] = i32x8{v[b][0][0], v[b][0][1], v[b][1][0], v[b][1][1], v[b][2][0], v[b][2][1], v[b][3][0], v[b][3][1]};
     }
   }
 };
 
-// acc += the product of two blocks over the 128 bytes of K in pieces 0 and 1.
+// acc += the product of two blocks over the 64 bytes of K in piece t (FP8: one
+// MFMA takes both pieces, with t = 0).
 template <class C>
-__device__ __forceinline__ void turn_mfma(typename C::Acc& acc, const i32x4 (&x)[2],
-                                          const i32x4 (&y)[2], int t) {
+__device__ __forceinline__ void turn_mfma(typename C::Acc& acc, const i32x8& x, const i32x8& y, int t) {
   if constexpr (C::TY == TY_FP8) {
-    // One MFMA takes both pieces.
     if (t == 0)
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-          __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7),
-          __builtin_shufflevector(y[0], y[1], 0, 1, 2, 3, 4, 5, 6, 7), acc, 0, 0, 0, 127, 0, 127);
-  } else if constexpr (C::TY == TY_I8) {
-    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[t], y[t], acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 0, 0, 0, 127, 0, 127);
   } else {
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[t]),
-                                                  __builtin_bit_cast(bf16x8, y[t]), acc, 0, 0, 0);
+    const i32x4 a = t == 0 ? low(x) : high(x), b = t == 0 ? low(y) : high(y);
+    if constexpr (C::TY == TY_I8)
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, acc, 0, 0, 0);
+    else
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                    __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
   }
 }
 
 // ---------------------------------------------------------------------- epilogue
 
+// What a tile's epilogue needs of its rows and columns, in LDS.
+struct TileVectors {
+  float scale_a[256], scale_b[256];
+  int zero_a[256], sum_b[256];
+  float bias[256];
+};
+
 // C = act(alpha * scale_a[m] * scale_b[n] * acc + beta * C + bias[n]) from the
 // registers. Lane l of block (i, j) holds row 16 i + l % 16 (in its half) and
-// the columns of TurnCfg::PAIR. row0, col0: the wave's first row and column.
-// ZERO: INT8 with zero points.
-template <class C, int ACT, bool ZERO>
+// the columns of TurnCfg::PAIR. c: the tile's first element; row0, col0: the
+// wave's first row and column in it. WHOLE: every row and column exists. ACT:
+// the activation, or -1: p.act.
+template <class C, int ACT, bool ZERO, bool WHOLE>
 __device__ __forceinline__ void turn_epilogue(const GemmArgs& p, const typename C::Acc (&acc)[8][4],
+                                              const TileVectors& tv, char* c, int rows, int cols,
                                               int row0, int col0, int lane) {
   constexpr bool SCALED = C::ES == 1;
   constexpr int W = C::PAIR ? 8 : 4;   // consecutive columns per store
   constexpr int RUNS = 16 / W;
+  constexpr int OB = C::OUT == OUT_F32 ? 4 : 2;
   const int q = lane >> 4, r = lane & 15;
   int n0[RUNS];
 #pragma unroll
   for (int s = 0; s < RUNS; ++s)
     n0[s] = col0 + (C::PAIR ? 128 * s + 8 * q : 128 * (s >> 1) + 16 * (s & 1) + 4 * q);
 
-  float cs[16], bias[16];
-  int zb[16];
+  // Rows inside, columns outside: the columns' vectors of one run at a time.
 #pragma unroll
-  for (int s = 0; s < RUNS; ++s)
+  for (int s = 0; s < RUNS; ++s) {
+    const int n = n0[s];
+    if (!WHOLE && n >= cols) continue;
+    const bool vec = WHOLE || n + W <= cols;
+    float cs[W], bias[W];
+    int zb[W];
 #pragma unroll
     for (int e = 0; e < W; ++e) {
-      const int n = n0[s] + e, x = s * W + e;
-      const bool in = n < p.N;
-      cs[x] = p.alpha;
-      if constexpr (SCALED) cs[x] = in ? p.alpha * p.scale_b[n] : 0.f;
-      bias[x] = p.bias && in ? bf16_bits_to_f32(p.bias[n]) : 0.f;
-      zb[x] = 0;
-      if (ZERO && in) zb[x] = p.sum_b[n];
+      cs[e] = p.alpha;
+      if constexpr (SCALED) cs[e] = p.alpha * tv.scale_b[n + e];
+      bias[e] = C::MODE != MODE_WGRAD && p.bias ? tv.bias[n + e] : 0.f;
+      zb[e] = 0;
+      if (ZERO) zb[e] = tv.sum_b[n + e];
     }
-  float sa[8];
-  int za[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int m = min(row0 + 128 * (i >> 2) + 16 * (i & 3) + r, p.M - 1);
-    sa[i] = 1.f;
-    za[i] = 0;
-    if constexpr (SCALED) sa[i] = p.scale_a[m];
-    if (ZERO) za[i] = p.zero_a[m];
-  }
-
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int m = row0 + 128 * (i >> 2) + 16 * (i & 3) + r;
-    if (m >= p.M) continue;
-#pragma unroll
-    for (int s = 0; s < RUNS; ++s) {
-      const int n = n0[s];
-      if (n >= p.N) continue;
-      const int64_t off = static_cast<int64_t>(m) * p.ldc + n;
-      const bool whole = n + W <= p.N;
+    for (int i = 0; i < 8; ++i) {
+      __builtin_amdgcn_sched_barrier(0);  // one run's registers at a time
+      const int m = row0 + 128 * (i >> 2) + 16 * (i & 3) + r;
+      if (!WHOLE && m >= rows) continue;
+      float sa = 1.f;
+      int za = 0;
+      if constexpr (SCALED) sa = tv.scale_a[m];
+      if (ZERO) za = tv.zero_a[m];
+      char* at = c + m * p.ldc * OB + n * OB;
       float v[W];
 #pragma unroll
       for (int e = 0; e < W; ++e) {
         const auto a = acc[i][C::PAIR ? 2 * s + (e >> 2) : s][e & 3];
         float z;
-        if constexpr (C::TY == TY_I8) z = i8_sum(a, ZERO, za[i], static_cast<double>(zb[s * W + e]));
+        if constexpr (C::TY == TY_I8) z = i8_sum(a, ZERO, za, static_cast<double>(zb[e]));
         else z = a;
-        v[e] = fmaf(z, SCALED ? sa[i] * cs[s * W + e] : cs[s * W + e], bias[s * W + e]);
+        v[e] = fmaf(z, SCALED ? sa * cs[e] : cs[e], bias[e]);
       }
       if (p.beta != 0.f) {
-        float c[W];
-        if (whole) {
+        float in[W];
+        if (vec) {
           if constexpr (C::OUT == OUT_BF16) {
-            const u32x4 h = *reinterpret_cast<const u32x4_at2*>(static_cast<const uint16_t*>(p.C) + off);
+            const u32x4 h = *reinterpret_cast<const u32x4_at2*>(at);
 #pragma unroll
             for (int e = 0; e < W; ++e)
-              c[e] = __uint_as_float(e & 1 ? h[e >> 1] & 0xffff0000u : h[e >> 1] << 16);
+              in[e] = __uint_as_float(e & 1 ? h[e >> 1] & 0xffff0000u : h[e >> 1] << 16);
           } else {
-            const f32x4 h = *reinterpret_cast<const f32x4_at4*>(static_cast<const float*>(p.C) + off);
+            const f32x4 h = *reinterpret_cast<const f32x4_at4*>(at);
 #pragma unroll
-            for (int e = 0; e < W; ++e) c[e] = h[e];
+            for (int e = 0; e < W; ++e) in[e] = h[e];
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < W; ++e) c[e] = n + e < p.N ? load_cin1<C::OUT>(p.C, off + e) : 0.f;
+          for (int e = 0; e < W; ++e) in[e] = n + e < cols ? load_cin1<C::OUT>(at, e) : 0.f;
         }
 #pragma unroll
-        for (int e = 0; e < W; ++e) v[e] = fmaf(p.beta, c[e], v[e]);
+        for (int e = 0; e < W; ++e) v[e] = fmaf(p.beta, in[e], v[e]);
       }
 #pragma unroll
-      for (int e = 0; e < W; ++e) v[e] = apply_act<C::OUT>(v[e], ACT);
-      if (whole) {
+      for (int e = 0; e < W; ++e) v[e] = apply_act<C::OUT>(v[e], ACT < 0 ? p.act : ACT);
+      if (vec) {
         if constexpr (C::OUT == OUT_BF16) {
           u32x4 h;
 #pragma unroll
           for (int e = 0; e < 4; ++e) h[e] = f32x2_to_bf16x2_bits(v[2 * e], v[2 * e + 1]);
-          __builtin_nontemporal_store(h, reinterpret_cast<u32x4_at2*>(static_cast<uint16_t*>(p.C) + off));
+          *reinterpret_cast<u32x4_at2*>(at) = h;
         } else {
-          __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]},
-                                      reinterpret_cast<f32x4_at4*>(static_cast<float*>(p.C) + off));
+          *reinterpret_cast<f32x4_at4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
         }
       } else {
 #pragma unroll
         for (int e = 0; e < W; ++e)
-          if (n + e < p.N) store_out1<C::OUT>(p.C, off + e, v[e], 1.f, 0.f);
+          if (n + e < cols) store_out1<C::OUT>(at, e, v[e], 1.f, 0.f);
       }
     }
   }
 }
 
-// Runs the epilogue with the activation as a compile-time parameter.
-template <class C, bool ZERO>
+// Runs the epilogue with the activation as a compile-time parameter where the
+// tile is whole.
+template <class C, bool ZERO, class... Rest>
 __device__ __forceinline__ void turn_epilogues(const GemmArgs& p, const typename C::Acc (&acc)[8][4],
-                                               int row0, int col0, int lane) {
-  const int act = p.act;
-  if (act == ACT_NONE) turn_epilogue<C, ACT_NONE, ZERO>(p, acc, row0, col0, lane);
-  else if (act == ACT_RELU) turn_epilogue<C, ACT_RELU, ZERO>(p, acc, row0, col0, lane);
-  else if (act == ACT_GELU_ERF) turn_epilogue<C, ACT_GELU_ERF, ZERO>(p, acc, row0, col0, lane);
-  else turn_epilogue<C, ACT_GELU_TANH, ZERO>(p, acc, row0, col0, lane);
+                                               bool whole, const Rest&... rest) {
+  if (!whole) {
+    turn_epilogue<C, -1, ZERO, false>(p, acc, rest...);
+  } else if constexpr (C::MODE == MODE_WGRAD) {
+    turn_epilogue<C, ACT_NONE, ZERO, true>(p, acc, rest...);
+  } else {
+    const int act = p.act;
+    if (act == ACT_NONE) turn_epilogue<C, ACT_NONE, ZERO, true>(p, acc, rest...);
+    else if (act == ACT_RELU) turn_epilogue<C, ACT_RELU, ZERO, true>(p, acc, rest...);
+    else if (act == ACT_GELU_ERF) turn_epilogue<C, ACT_GELU_ERF, ZERO, true>(p, acc, rest...);
+    else turn_epilogue<C, ACT_GELU_TANH, ZERO, true>(p, acc, rest...);
+  }
 }
 
 // ------------------------------------------------------------------------ kernel
@@ -357,88 +409,162 @@ __device__ __forceinline__ void turn_barrier() {
   fence();
 }
 
+// One tile's work: its operands from its first row and column on.
+struct TurnTile {
+  const char* A;
+  const char* B;
+  char* C;
+  int rows, cols, K;
+  int slices;             // even: a last slice past K adds zeros
+  int64_t row, col;       // first row of scale_a / zero_a, first element of scale_b, bias, sum_b
+};
+
+// Everything a workgroup keeps in LDS: the operands' slices (A's, then B's),
+// the vectors of two tiles (the one whose copies run and the one before), the
+// groups' tiles, and the last chunks of a K that ends inside one.
+struct TurnShared {
+  char ring[131072];
+  TileVectors vectors[2];
+  GroupTable groups;
+  uint4 tail[512];
+};
+static_assert(sizeof(TurnShared) <= 160 * 1024, "LDS budget");
+
+// The workgroup's tile number `v`, or its next one if there is none of that number (false: no more).
+template <class C>
+__device__ __forceinline__ bool turn_tile(const GemmArgs& p, const TurnShared& sh, int nwg, int& v, int lane,
+                                          TurnTile& t) {
+  if (v >= nwg) return false;
+  constexpr int OB = C::OUT == OUT_F32 ? 4 : 2;
+  int tm, tn, rows = p.M, K = p.K;
+  int64_t r0 = 0;  // first row of the group
+  const char* A = static_cast<const char*>(p.A);
+  const char* B = static_cast<const char*>(p.B);
+  char* c = static_cast<char*>(p.C);
+  t.col = 0;
+  if constexpr (C::MODE == MODE_DENSE) {
+    tile_coords(xcd_remap(v, nwg), p.tiles_m, p.tiles_n, 4, tm, tn);
+  } else if constexpr (C::MODE == MODE_GROUPED) {
+    const int L = xcd_remap(v, nwg);
+    int g, s, tiles, first;
+    find_in_table(sh.groups, L / p.tiles_n, p.groups, lane, g, s, rows, tiles, first);
+    tile_coords(L - first * p.tiles_n, tiles, p.tiles_n, kGroupedBand, tm, tn);
+    r0 = s;
+    B += g * p.stride_b * C::ES;
+    t.col = static_cast<int64_t>(g) * p.N;
+  } else {
+    int g, s, e;
+    while (!wgrad_tile(p, v, g, tm, tn))
+      if ((v += gridDim.x) >= nwg) return false;
+    group_rows(p, g, s, e);
+    s = __builtin_amdgcn_readfirstlane(s);
+    K = __builtin_amdgcn_readfirstlane(e) - s;
+    A += s * p.lda * C::ES;
+    B += s * p.ldb * C::ES;
+    c += g * p.stride_b * OB;
+  }
+  const int m0 = tm * 256, n0 = tn * 256;
+  t.rows = min(rows - m0, 256);
+  t.cols = min(p.N - n0, 256);
+  t.row = r0 + m0;
+  t.col += n0;
+  t.A = A + t.row * (C::AR ? 1 : p.lda) * C::ES;
+  t.B = B + n0 * (C::BR ? 1 : p.ldb) * C::ES;
+  t.C = c + (t.row * p.ldc + n0) * OB;
+  t.K = K;
+  t.slices = 2 * max(1, (K + 2 * C::BKE - 1) / (2 * C::BKE));
+  return true;
+}
+
+// The same value through a move that the optimiser cannot look through: what
+// is computed from it stays where it is used, instead of being hoisted out of
+// the loop over tiles, where it would hold a register throughout.
+__device__ __forceinline__ int opaque(int x) {
+  int y;
+  asm volatile("v_mov_b32 %0, %1" : "=v"(y) : "v"(x));
+  return y;
+}
+
 template <class C>
 __global__ void __launch_bounds__(kTurnThreads, 2) gemm_turn_kernel(GemmArgs p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __shared__ __attribute__((aligned(1024))) char smem[131072];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ __attribute__((aligned(1024))) TurnShared sh;
+  char* const smem = sh.ring;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  int tm, tn;
-  if constexpr (C::MODE == MODE_DENSE) {
-    tile_coords(xcd_remap(blockIdx.x, gridDim.x), p.tiles_m, p.tiles_n, 4, tm, tn);
-  } else if constexpr (C::MODE == MODE_GROUPED) {
-    int L, g, s, rows, tiles, first;
-    if (!find_group<256>(p, blockIdx.x, lane, L, g, s, rows, tiles, first)) return;
-    tile_coords(L - first * p.tiles_n, tiles, p.tiles_n, kGroupedBand, tm, tn);
-    // The operands of this row tile alone, its first row as row 0: 64-bit
-    // pointer arithmetic here, so that 32-bit offsets never see more than a
-    // tile's rows or one group's weight.
-    const int r0 = s + tm * 256;
-    p.A = static_cast<const char*>(p.A) + r0 * p.lda * C::ES;
-    p.C = static_cast<char*>(p.C) + r0 * p.ldc * (C::OUT == OUT_F32 ? 4 : 2);
-    p.M = min(rows - tm * 256, 256);
-    tm = 0;
-    p.B = static_cast<const char*>(p.B) + g * p.stride_b * C::ES;
-    const int64_t gn = static_cast<int64_t>(g) * p.N;
-    if (p.bias) p.bias += gn;
-    if constexpr (C::ES == 1) {
-      p.scale_a += r0;
-      p.scale_b += gn;
-      if (p.zero_a) {
-        p.zero_a += r0;
-        p.sum_b += gn;
-      }
-    }
-  } else {
-    int g, s, e;
-    if (!wgrad_tile(p, blockIdx.x, g, tm, tn)) return;
-    group_rows(p, g, s, e);
-    p.K = __builtin_amdgcn_readfirstlane(e - s);
-    s = __builtin_amdgcn_readfirstlane(s);
-    p.A = static_cast<const char*>(p.A) + s * p.lda * C::ES;
-    p.B = static_cast<const char*>(p.B) + s * p.ldb * C::ES;
-    p.C = static_cast<char*>(p.C) + g * p.stride_b * (C::OUT == OUT_F32 ? 4 : 2);
+  // A workgroup takes tiles v, v + gridDim.x, ... as one stream of slices: the
+  // copies run ahead into the next tile, so that neither a tile's start nor
+  // its stores leave the matrix cores without operands.
+  int v = blockIdx.x, nwg = p.turn_tiles;
+  if constexpr (C::MODE == MODE_GROUPED) {
+    fill_table<256>(p, sh.groups, wave, lane);
+    __syncthreads();
+    nwg = __builtin_amdgcn_readfirstlane(sh.groups.row_tiles) * p.tiles_n;
   }
-  const int m0 = tm * 256, n0 = tn * 256, k_end = p.K;
-  const int nk = (k_end + C::BKE - 1) / C::BKE;
+  TurnTile cur, nxt;
+  bool more = turn_tile<C>(p, sh, nwg, v, lane, cur);
+  if (!more) return;
 
   std::conditional_t<C::AR, RowsCopy<C, false>, KMajorCopy<C, false>> ca;
   std::conditional_t<C::BR, RowsCopy<C, C::PAIR>, KMajorCopy<C, C::PAIR>> cb;
-  ca.init(p.A, p.lda, m0, p.M, p.K, wave, lane);
-  cb.init(p.B, p.ldb, n0, p.N, p.K, wave, lane);
   Fragments<C, 4, C::AR, false> ra;
   Fragments<C, 2, C::BR, C::PAIR> rb;
-  ra.init(0, 64 * (wave >> 2), lane);
-  rb.init(kBBase, 32 * (wave & 3), lane);
+
+  // The copies' place in the stream: K0 of their slice, and what is left of their tile.
+  int ck0 = 0, cK = 0, cleft = 0;
+  const auto point = [&](const TurnTile& t) __attribute__((always_inline)) {
+    const int l = opaque(lane);
+    ca.point(t.A, p.lda, t.rows, t.K, wave, l);
+    cb.point(t.B, p.ldb, t.cols, t.K, wave, l);
+    ck0 = 0;
+    cK = t.K;
+    cleft = t.slices;
+  };
+  // A tile's vectors pass through three registers of a thread (the first 256
+  // threads: its rows' and the bias, the others: its columns').
+  constexpr bool VECTORS = C::MODE != MODE_WGRAD;
+  float vec0 = 0.f, vec2 = 0.f;
+  int vec1 = 0;
+  const auto load_vectors = [&](const TurnTile& t) __attribute__((always_inline)) {
+    const int id = opaque(tid);
+    const bool of_a = id < 256;
+    const int x = id & 255;
+    if constexpr (C::ES == 1) {
+      const bool in = x < (of_a ? t.rows : t.cols);
+      if (in) vec0 = of_a ? p.scale_a[t.row + x] : p.scale_b[t.col + x];
+      if constexpr (C::TY == TY_I8) {
+        if (p.zero_a && in) vec1 = of_a ? p.zero_a[t.row + x] : p.sum_b[t.col + x];
+      }
+    }
+    if (p.bias && of_a && x < t.cols) vec2 = bf16_bits_to_f32(p.bias[t.col + x]);
+  };
+  const auto store_vectors = [&](TileVectors& tv) __attribute__((always_inline)) {
+    const int id = opaque(tid), x = id & 255;
+    if constexpr (C::ES == 1) {
+      (id < 256 ? tv.scale_a : tv.scale_b)[x] = vec0;
+      if constexpr (C::TY == TY_I8) (id < 256 ? tv.zero_a : tv.sum_b)[x] = vec1;
+    }
+    if (id < 256) tv.bias[x] = vec2;
+  };
 
   typename C::Acc acc[8][4];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = typename C::Acc{0, 0, 0, 0};
-  i32x4 fa[4][2], fb[2][2][2];
-
-  auto copy_a = [&](int buf, int h, int s) __attribute__((always_inline)) {
-    ca.issue(smem + buf * kBuf + h * kHalf, h, wave, s * C::BKE, k_end);
+  i32x8 fa[4], fb[2][2];
+  const auto copy_a = [&](int buf, int h) __attribute__((always_inline)) {
+    ca.issue(smem + buf * kBuf + h * kHalf, h, wave, ck0, cK);
   };
-  auto copy_b = [&](int buf, int h, int s) __attribute__((always_inline)) {
-    cb.issue(smem + kBBase + buf * kBuf + h * kHalf, h, wave, s * C::BKE, k_end);
+  const auto copy_b = [&](int buf, int h) __attribute__((always_inline)) {
+    cb.issue(smem + kBBase + buf * kBuf + h * kHalf, h, wave, ck0, cK);
   };
-  auto read_a = [&](int buf, int h) __attribute__((always_inline)) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) fa[b][t] = ra.read(smem, buf * kBuf + h * kHalf, b, t);
+  const auto read_a = [&](auto buf, auto h) __attribute__((always_inline)) {
+    ra.template read<decltype(buf)::value * kBuf + decltype(h)::value * kHalf>(fa);
   };
-  auto read_b = [&](int buf, int h) __attribute__((always_inline)) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) fb[h][b][t] = rb.read(smem, buf * kBuf + h * kHalf, b, t);
+  const auto read_b = [&](auto buf, auto h) __attribute__((always_inline)) {
+    constexpr int H = decltype(h)::value;
+    rb.template read<decltype(buf)::value * kBuf + H * kHalf>(fb[H]);
   };
   // The second half of a turn: the quarter (ha, hb), between two barriers.
-  auto multiply = [&](int ha, int hb) __attribute__((always_inline)) {
+  const auto multiply = [&](int ha, int hb) __attribute__((always_inline)) {
     fence();
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kAhead) : "memory");
     turn_barrier();
@@ -449,62 +575,111 @@ __global__ void __launch_bounds__(kTurnThreads, 2) gemm_turn_kernel(GemmArgs p) 
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           turn_mfma<C>(acc[4 * ha + i][2 * hb + j], fb[hb][j], fa[i], t);
+    // (Keeps the products on this side of the barrier: they touch no memory.)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(acc[4 * ha + i][2 * hb + j]));
     // This turn's reads are done: from the next turn but one their LDS may be refilled.
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     turn_barrier();
   };
-  // Slice s in buffer f; half f of its B is in registers, and turn 4 reads the
-  // half that the next slice starts with.
-  auto slice = [&](const int f, int s) __attribute__((always_inline)) {
-    read_a(f, 0);
-    copy_a(1 - f, 1, s + 1);
+  int parity = 0;  // of the tile whose copies run
+  bool moved = false;
+  // A slice in buffer f; half f of its B is in registers, and turn 4 reads the
+  // half that the next slice starts with. A tile has an even number of slices,
+  // so the copies pass from one tile to the next in slices of buffer 0.
+  using Zero = std::integral_constant<int, 0>;
+  using One = std::integral_constant<int, 1>;
+  const auto advance = [&]() __attribute__((always_inline)) {
+    ck0 += C::BKE;
+    --cleft;
+    ca.next();
+    cb.next();
+  };
+  const auto slice = [&](auto F) __attribute__((always_inline)) {
+    constexpr int f = decltype(F)::value;
+    const std::integral_constant<int, 1 - f> G{};
+    copy_a(1 - f, 1);
+    read_a(F, Zero{});
+    advance();
+    if (f == 0) {
+      moved = cleft == 0;
+      if (moved) {
+        v += gridDim.x;
+        more = turn_tile<C>(p, sh, nwg, v, opaque(lane), nxt);
+        if (!more) {
+          nxt = cur;
+          nxt.K = 0;  // copies of zeros
+          nxt.slices = 1 << 30;
+        }
+        point(nxt);
+        if (VECTORS && more) load_vectors(nxt);
+      }
+    }
     multiply(0, f);
-    read_b(f, 1 - f);
-    copy_b(f, f, s + 2);
+    copy_b(f, f);
+    read_b(F, G);
+    if (VECTORS && f == 1 && moved) {
+      parity ^= 1;
+      store_vectors(sh.vectors[parity]);
+    }
     multiply(0, 1 - f);
-    read_a(f, 1);
-    copy_a(f, 0, s + 2);
+    copy_a(f, 0);
+    read_a(F, One{});
     multiply(1, 1 - f);
-    read_b(1 - f, 1 - f);
-    copy_b(f, 1 - f, s + 2);
+    copy_b(f, 1 - f);
+    read_b(G, G);
     multiply(1, f);
   };
 
-  if (nk > 0) {
-    // The copies that the turns before slice 0 would have issued, in their order.
-    copy_b(0, 0, 0);
-    copy_a(0, 0, 0);
-    copy_b(0, 1, 0);
-    copy_a(0, 1, 0);
-    copy_b(1, 1, 1);
-    copy_a(1, 0, 1);
-    copy_b(1, 0, 1);
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kAhead) : "memory");
-    turn_barrier();
-    read_b(0, 0);
+  // The copies that the turns before slice 0 would have issued, in their order.
+  point(cur);
+  if (VECTORS) {
+    load_vectors(cur);
+    store_vectors(sh.vectors[0]);
+  }
+  copy_b(0, 0);
+  copy_a(0, 0);
+  copy_b(0, 1);
+  copy_a(0, 1);
+  advance();
+  copy_b(1, 1);
+  copy_a(1, 0);
+  copy_b(1, 0);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kAhead) : "memory");
+  turn_barrier();
+  if (wave >= 4) turn_barrier();  // half a turn behind waves 0-3
+
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = typename C::Acc{0, 0, 0, 0};
+    // (Addresses of fragments are not held over an epilogue either.)
+    const int fl = opaque(lane);
+    const int lds = static_cast<int>(reinterpret_cast<uintptr_t>((G355_LDS char*)smem));
+    ra.init(lds, 64 * (wave >> 2), fl);
+    rb.init(lds + kBBase, 32 * (wave & 3), fl);
+    // Half 0 of B, read again so that no register holds it over an epilogue.
+    read_b(Zero{}, Zero{});
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (wave >= 4) turn_barrier();  // half a turn behind waves 0-3
-    int s = 0;
-    for (; s + 1 < nk; s += 2) {
-      slice(0, s);
-      slice(1, s + 1);
+    for (int s = 0; s < cur.slices; s += 2) {
+      slice(Zero{});
+      slice(One{});
     }
-    if (s < nk) slice(0, s);
-    if (wave < 4) turn_barrier();
-    // Copies past the end (of zeros) may still be writing LDS.
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    turn_barrier();
     // K ends inside a 16-byte chunk of K-major rows: no copy took that chunk,
     // as its bytes past the end may lie past the allocation. One thread per
     // row of A and of B writes it to LDS, zeros after its nb valid bytes, and
     // one more product is added whose other chunks are zero.
-    if (!C::AR && k_end % C::CE != 0) {
-      const int t = threadIdx.x;
-      const bool is_a = t < 256;
-      const int tail = k_end % C::CE, nb = tail * C::ES;
-      const int row = min((is_a ? m0 : n0) + (t & 255), (is_a ? p.M : p.N) - 1);
-      const uintptr_t src = reinterpret_cast<uintptr_t>(is_a ? p.A : p.B) +
-                            (row * (is_a ? p.lda : p.ldb) + k_end - tail) * C::ES;
+    const int tail = C::AR ? 0 : cur.K % C::CE;
+    if (tail != 0) {
+      const int id = opaque(tid);
+      const bool is_a = id < 256;
+      const int nb = tail * C::ES;
+      const int row = min(id & 255, (is_a ? cur.rows : cur.cols) - 1);
+      const uintptr_t src = reinterpret_cast<uintptr_t>(is_a ? cur.A : cur.B) +
+                            (row * (is_a ? p.lda : p.ldb) + cur.K - tail) * C::ES;
       // Only 4-byte aligned words that hold a valid byte are read.
       const uint32_t* word = reinterpret_cast<const uint32_t*>(src & ~uintptr_t{3});
       const int shift = static_cast<int>(src & 3), words = C::BR && !is_a ? 0 : (shift + nb + 3) >> 2;
@@ -513,53 +688,56 @@ __global__ void __launch_bounds__(kTurnThreads, 2) gemm_turn_kernel(GemmArgs p) 
       for (int i = 0; i < 5; ++i) d[i] = i < words ? word[i] : 0u;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t v = __builtin_amdgcn_alignbyte(d[i + 1], d[i], shift);
+        const uint32_t x = __builtin_amdgcn_alignbyte(d[i + 1], d[i], shift);
         const int keep = nb - 4 * i;
-        w[i] = keep >= 4 ? v : keep <= 0 ? 0u : (v & ((1u << (8 * keep)) - 1u));
+        w[i] = keep >= 4 ? x : keep <= 0 ? 0u : (x & ((1u << (8 * keep)) - 1u));
       }
       if (C::BR && !is_a) {
         // A column of B whose rows run along K: one element of each row.
-        const uint16_t* col = static_cast<const uint16_t*>(p.B) + row;
+        const uint16_t* col = reinterpret_cast<const uint16_t*>(cur.B) + row;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (i < tail) w[i >> 1] |= static_cast<uint32_t>(col[(k_end - tail + i) * p.ldb]) << (16 * (i & 1));
+          if (i < tail) w[i >> 1] |= static_cast<uint32_t>(col[(cur.K - tail + i) * p.ldb]) << (16 * (i & 1));
       }
-      *reinterpret_cast<uint4*>(smem + t * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      sh.tail[id] = make_uint4(w[0], w[1], w[2], w[3]);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      turn_barrier();  // two: waves 4-7 are one barrier behind
       turn_barrier();
       // Row d of block b of half h as in Fragments.
-      const int d16 = lane & 15;
+      const int l = id & 63, d16 = l & 15;
       const auto chunk = [&](int r) {
-        i32x4 v = *reinterpret_cast<const i32x4*>(smem + r * 16);
+        i32x4 x = *reinterpret_cast<const i32x4*>(&sh.tail[r]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = lane < 16 ? v[i] : 0;
-        return v;
+        for (int i = 0; i < 4; ++i) x[i] = l < 16 ? x[i] : 0;
+        return __builtin_shufflevector(x, i32x4{0, 0, 0, 0}, 0, 1, 2, 3, 4, 5, 6, 7);
       };
       const int rowb = 256 + 32 * (wave & 3) + (C::PAIR ? 8 * (d16 >> 2) + (d16 & 3) : d16);
+      // (The fragments in registers belong to the next tile.)
+      i32x8 y[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          fb[h][b][0] = chunk(rowb + 128 * h + (C::PAIR ? 4 : 16) * b);
-          fb[h][b][1] = i32x4{0, 0, 0, 0};
-        }
+      for (int j = 0; j < 4; ++j) y[j] = chunk(rowb + 128 * (j >> 1) + (C::PAIR ? 4 : 16) * (j & 1));
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const i32x4 x[2] = {chunk(64 * (wave >> 2) + 128 * (i >> 2) + 16 * (i & 3) + d16), i32x4{0, 0, 0, 0}};
+        const i32x8 x = chunk(64 * (wave >> 2) + 128 * (i >> 2) + 16 * (i & 3) + d16);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) turn_mfma<C>(acc[i][j], fb[j >> 1][j & 1], x, 0);
+        for (int j = 0; j < 4; ++j) turn_mfma<C>(acc[i][j], y[j], x, 0);
       }
     }
-  }
 
-  const int row0 = m0 + 64 * (wave >> 2), col0 = n0 + 32 * (wave & 3);
-  if constexpr (C::TY == TY_I8) {
-    if (p.zero_a) {
-      turn_epilogues<C, true>(p, acc, row0, col0, lane);
-      return;
-    }
+    const bool whole = cur.rows == 256 && cur.cols == 256;
+    const TileVectors& tv = sh.vectors[parity ^ 1];
+    const int row0 = 64 * (wave >> 2), col0 = 32 * (wave & 3), l = opaque(lane);
+    bool zero = false;
+    if constexpr (C::TY == TY_I8) zero = p.zero_a != nullptr;
+    if (zero) turn_epilogues<C, C::TY == TY_I8>(p, acc, whole, tv, cur.C, cur.rows, cur.cols, row0, col0, l);
+    else turn_epilogues<C, false>(p, acc, whole, tv, cur.C, cur.rows, cur.cols, row0, col0, l);
+    fence();
+    if (!more) break;
+    cur = nxt;
   }
-  turn_epilogues<C, false>(p, acc, row0, col0, lane);
+  if (wave < 4) turn_barrier();
+  // Copies of zeros may still be on their way into LDS.
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #endif
 }
 
@@ -567,8 +745,10 @@ __global__ void __launch_bounds__(kTurnThreads, 2) gemm_turn_kernel(GemmArgs p) 
 
 template <class C>
 static hipError_t go(int64_t grid, const GemmArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((gemm_turn_kernel<C>), dim3(static_cast<unsigned>(grid)), dim3(kTurnThreads), 0,
-                     stream, a);
+  GemmArgs t = a;
+  t.turn_tiles = static_cast<int>(grid);
+  hipLaunchKernelGGL((gemm_turn_kernel<C>), dim3(static_cast<unsigned>(grid < kTurnGrid ? grid : kTurnGrid)),
+                     dim3(kTurnThreads), 0, stream, t);
   return hipGetLastError();
 }
 

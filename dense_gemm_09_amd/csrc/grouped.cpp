@@ -46,7 +46,7 @@ GroupedPlan plan_grouped(int64_t G, int64_t T, int64_t N, bool bytes1) {
       const double wgs = groups * (avg / b + 0.5) * static_cast<double>(ceil_div(N, b));
       return std::max(1.0, wgs / (kCUs * occupancy)) * b * b * occupancy / eff;
     };
-    if (cost(256, 1, 0.85) < cost(128, 2, bytes1 ? 0.80 : 0.67)) best = {256, 256, 0};
+    if (G <= kTableGroups && cost(256, 1, 0.85) < cost(128, 2, bytes1 ? 0.80 : 0.67)) best = {256, 256, 0};
   }
   best.grid = most_row_tiles(G, T, best.bm) * ceil_div(N, best.bn);
   return best;

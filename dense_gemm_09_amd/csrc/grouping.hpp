@@ -89,6 +89,56 @@ __device__ __forceinline__ bool find_group(const GemmArgs& p, int b, int lane, i
   return false;  // not reached: rt < all
 }
 
+// The groups' row tiles as a table in LDS, for workgroups that take many tiles.
+struct GroupTable {
+  int begin[kTableGroups], end[kTableGroups];  // rows
+  int tiles[kTableGroups];                     // row tiles up to and with this group
+  int row_tiles;                               // in all; 0 where the offsets count more than the launch has
+};
+
+// Filled by wave 0 (the caller's barrier follows).
+template <int BM>
+__device__ __forceinline__ void fill_table(const GemmArgs& p, GroupTable& t, int wave, int lane) {
+  if (wave != 0) return;
+  int before = 0;
+  bool fits = true;
+  for (int c = 0; c < p.groups; c += 64) {
+    int s = 0, e = 0;
+    if (c + lane < p.groups) group_rows(p, c + lane, s, e);
+    int n = (e - s + BM - 1) / BM;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int x = __shfl_up(n, o);
+      n += lane >= o ? x : 0;
+    }
+    t.begin[c + lane] = s;
+    t.end[c + lane] = e;
+    t.tiles[c + lane] = before + n;
+    before += __builtin_amdgcn_readlane(n, 63);
+    // Offsets that decrease can count more tiles than the groups can have.
+    fits = fits && static_cast<int64_t>(before) * p.tiles_n <= p.turn_tiles;
+    if (!fits) break;
+  }
+  if (lane == 0) t.row_tiles = fits ? before : 0;
+}
+
+// The group of row tile `rt` < row_tiles, as in find_group.
+__device__ __forceinline__ void find_in_table(const GroupTable& t, int rt, int groups, int lane, int& g, int& s,
+                                              int& rows, int& tiles, int& first) {
+  int c = 0, end = 0;
+  unsigned long long hit = 0;
+  for (; c < groups; c += 64) {
+    end = t.tiles[c + lane];
+    hit = __ballot(end > rt);
+    if (hit != 0) break;
+  }
+  g = c + __builtin_ctzll(hit);
+  first = __builtin_amdgcn_readfirstlane(g > 0 ? t.tiles[g - 1] : 0);
+  tiles = __builtin_amdgcn_readfirstlane(t.tiles[g]) - first;
+  s = __builtin_amdgcn_readfirstlane(t.begin[g]);
+  rows = __builtin_amdgcn_readfirstlane(t.end[g]) - s;
+}
+
 // The tile of workgroup `b` of a weight gradient: every group has the same
 // tiles, and the groups differ in their K range. Each XCD takes an eighth of
 // every group's tiles, neighbours of each other, so that groups of unequal
