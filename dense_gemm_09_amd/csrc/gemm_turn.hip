@@ -287,8 +287,8 @@ struct TileVectors {
 // C = act(alpha * scale_a[m] * scale_b[n] * acc + beta * C + bias[n]) from the
 // registers. Lane l of block (i, j) holds row 16 i + l % 16 (in its half) and
 // the columns of TurnCfg::PAIR. c: the tile's first element; row0, col0: the
-// wave's first row and column in it. WHOLE: every row and column exists. ACT:
-// the activation, or -1: p.act.
+// wave's first row and column in it. WHOLE: every column exists. ACT: the
+// activation, or -1: p.act.
 template <class C, int ACT, bool ZERO, bool WHOLE>
 __device__ __forceinline__ void turn_epilogue(const GemmArgs& p, const typename C::Acc (&acc)[8][4],
                                               const TileVectors& tv, char* c, int rows, int cols,
@@ -323,7 +323,7 @@ __device__ __forceinline__ void turn_epilogue(const GemmArgs& p, const typename 
     for (int i = 0; i < 8; ++i) {
       __builtin_amdgcn_sched_barrier(0);  // one run's registers at a time
       const int m = row0 + 128 * (i >> 2) + 16 * (i & 3) + r;
-      if (!WHOLE && m >= rows) continue;
+      if (m >= rows) continue;
       float sa = 1.f;
       int za = 0;
       if constexpr (SCALED) sa = tv.scale_a[m];
@@ -378,13 +378,13 @@ __device__ __forceinline__ void turn_epilogue(const GemmArgs& p, const typename 
   }
 }
 
-// Runs the epilogue with the activation as a compile-time parameter where the
-// tile is whole.
+// Runs the epilogue with the activation as a compile-time parameter where
+// every column exists.
 template <class C, bool ZERO, class... Rest>
 __device__ __forceinline__ void turn_epilogues(const GemmArgs& p, const typename C::Acc (&acc)[8][4],
                                                bool whole, const Rest&... rest) {
   if (!whole) {
-    turn_epilogue<C, -1, ZERO, false>(p, acc, rest...);
+    turn_epilogue<C, C::MODE == MODE_WGRAD ? static_cast<int>(ACT_NONE) : -1, ZERO, false>(p, acc, rest...);
   } else if constexpr (C::MODE == MODE_WGRAD) {
     turn_epilogue<C, ACT_NONE, ZERO, true>(p, acc, rest...);
   } else {
@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(kTurnThreads, 2) gemm_turn_kernel(GemmArgs p) 
       }
     }
 
-    const bool whole = cur.rows == 256 && cur.cols == 256;
+    const bool whole = cur.cols == 256;
     const TileVectors& tv = sh.vectors[parity ^ 1];
     const int row0 = 64 * (wave >> 2), col0 = 32 * (wave & 3), l = opaque(lane);
     bool zero = false;
