@@ -902,6 +902,28 @@ gemm_tile_kernel(GemmArgs p) {
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
 
+  // The same for two blocks, written out with the wait for them: before the
+  // compiler's own form of these reads it waits for every copy in flight. (The
+  // dense kernels keep the form they were measured with.)
+  constexpr bool OWN_TR = MODE != MODE_DENSE;
+  auto read_tr2 = [&](const char* p0, const char* p1, auto rown, auto& f0, auto& f1) __attribute__((always_inline)) {
+    typedef int i32x2 __attribute__((ext_vector_type(2)));
+    i32x2 a0, a1, b0, b1;
+    const int q0 = static_cast<int>(reinterpret_cast<uintptr_t>((G355_LDS const char*)p0));
+    const int q1 = static_cast<int>(reinterpret_cast<uintptr_t>((G355_LDS const char*)p1));
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4\n\tds_read_b64_tr_b16 %1, %4 offset:%6\n\t"
+        "ds_read_b64_tr_b16 %2, %5\n\tds_read_b64_tr_b16 %3, %5 offset:%6\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(a0), "=&v"(a1), "=&v"(b0), "=&v"(b1)
+        : "v"(q0), "v"(q1), "n"(4 * decltype(rown)::value)
+        : "memory");
+    if constexpr (!C::FP8) {
+      f0 = __builtin_bit_cast(FragOf<C>, i32x4{a0[0], a0[1], a1[0], a1[1]});
+      f1 = __builtin_bit_cast(FragOf<C>, i32x4{b0[0], b0[1], b1[0], b1[1]});
+    }
+  };
+
   typename C::Acc acc[C::FM][C::FN];
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
@@ -921,15 +943,29 @@ gemm_tile_kernel(GemmArgs p) {
     const char* bt = b_tile(st);
     if constexpr (!C::FP8) {
       const int co = ((2 * t + half) ^ sw) << 4;
+      if constexpr (A_ROWS && OWN_TR) {
+#pragma unroll
+        for (int i = 0; i < C::FM; i += 2)
+          read_tr2(at + atr_row + atr_col[i] + (16 * t) * ROWN_A, at + atr_row + atr_col[i + 1] + (16 * t) * ROWN_A,
+                   std::integral_constant<int, ROWN_A>{}, fa[i], fa[i + 1]);
+      }
+      if constexpr (B_ROWS && OWN_TR) {
+#pragma unroll
+        for (int j = 0; j < C::FN; j += 2)
+          read_tr2(bt + ntr_row + ntr_col[j] + (16 * t) * ROWN_B, bt + ntr_row + ntr_col[j + 1] + (16 * t) * ROWN_B,
+                   std::integral_constant<int, ROWN_B>{}, fb[j], fb[j + 1]);
+      }
 #pragma unroll
       for (int i = 0; i < C::FM; ++i) {
-        if constexpr (A_ROWS)
+        if constexpr (A_ROWS && OWN_TR) continue;
+        else if constexpr (A_ROWS)
           fa[i] = __builtin_bit_cast(
               Frag, read_tr(at + atr_row + atr_col[i] + (16 * t) * ROWN_A, ROWN_A));
         else
           fa[i] = *reinterpret_cast<const Frag*>(at + a_row + i * 32 * C::ROWB + co);
       }
-      if constexpr (B_ROWS) {
+      if constexpr (B_ROWS && OWN_TR) {
+      } else if constexpr (B_ROWS) {
 #pragma unroll
         for (int j = 0; j < C::FN; ++j)
           fb[j] = __builtin_bit_cast(
@@ -1015,7 +1051,8 @@ gemm_tile_kernel(GemmArgs p) {
   // LDS fragment reads per k-step (an N-major B block takes two 8-byte
   // transposing reads).
   constexpr int READS =
-      C::FP8 ? 2 * (C::FM + C::FN) : (A_ROWS ? 2 : 1) * C::FM + (B_ROWS ? 2 : 1) * C::FN;
+      C::FP8 ? 2 * (C::FM + C::FN)
+             : (A_ROWS ? (OWN_TR ? 0 : 2) : 1) * C::FM + (B_ROWS ? (OWN_TR ? 0 : 2) : 1) * C::FN;
   constexpr int MFMAS = C::FM * C::FN;
   constexpr bool ALL_DMA = LA != LOAD_GENERIC && LB != LOAD_GENERIC;
   // With both operands on the DMA path, the loads of slice s are issued in
@@ -1352,6 +1389,13 @@ using BigI8 = CfgI8<256, 256, 2, 4, 2, 3>;
 using SmallI8 = CfgI8<128, 128, 2, 2, 2>;
 using ThinI8 = CfgI8<64, 256, 1, 4, 4>;
 using NarrowI8 = CfgI8<64, 128, 1, 2, 6>;
+// 128x128 with a ring of four slices (128 KB, one workgroup per CU), for
+// launches whose workgroups do not share a CU anyway: three slices in flight
+// instead of one.
+using Deep16 = TileCfg<128, 128, 2, 2, false, 128, 4>;
+using Deep8 = TileCfg<128, 128, 2, 2, true, 128, 4>;
+using DeepI8 = CfgI8<128, 128, 2, 2, 4>;
+constexpr int64_t kDeepGrid = 256;
 
 #if defined(G355_I8)
 
@@ -1366,18 +1410,21 @@ hipError_t G355_I8_LAUNCHER(G355_RAGGED, G355_PART)(const Plan& plan, const Laun
   if (plan.bm == 64)
     return plan.bn == 256 ? launch_cfg<ThinI8, LOAD_DIRECT, LOAD_DIRECT, R>(plan, spec, a, stream)
                           : launch_cfg<NarrowI8, LOAD_DIRECT, LOAD_DIRECT, R>(plan, spec, a, stream);
+  if (plan.bm == 128 && plan.grid <= kDeepGrid)
+    return launch_cfg<DeepI8, LOAD_DIRECT, LOAD_DIRECT, R>(plan, spec, a, stream);
   return plan.bm == 256 ? launch_cfg<BigI8, LOAD_DIRECT, LOAD_DIRECT, R>(plan, spec, a, stream)
                         : launch_cfg<SmallI8, LOAD_DIRECT, LOAD_DIRECT, R>(plan, spec, a, stream);
 }
 
 #elif defined(G355_GROUPED)
 
-// One element type's tiles: 128x128, and 64x128 with a deep ring.
-template <class SMALL, class NARROW, int LB>
+// One element type's tiles: 128x128 (with a deep ring where a CU has one workgroup), and 64x128.
+template <class SMALL, class DEEP, class NARROW, int LB>
 static hipError_t launch_grouped_type(const GroupedPlan& plan, const GemmArgs& a,
                                       hipStream_t stream) {
   constexpr bool R = G355_RAGGED != 0;
   if (plan.bm == 64) return launch_grouped<NARROW, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
+  if (plan.grid <= kDeepGrid) return launch_grouped<DEEP, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
   return launch_grouped<SMALL, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
 }
 
@@ -1394,11 +1441,11 @@ hipError_t G355_GROUPED_LAUNCHER(G355_RAGGED, G355_PART)(const GroupedPlan& plan
     else
       return launch_grouped<Small16, LOAD_GENERIC, LOAD_GENERIC, false, MODE_GROUPED>(plan.grid, a, stream);
   }
-  if (spec.i8) return launch_grouped_type<SmallI8, NarrowI8, LOAD_DIRECT>(plan, a, stream);
-  if (spec.fp8) return launch_grouped_type<Small8, Narrow8, LOAD_DIRECT>(plan, a, stream);
+  if (spec.i8) return launch_grouped_type<SmallI8, DeepI8, NarrowI8, LOAD_DIRECT>(plan, a, stream);
+  if (spec.fp8) return launch_grouped_type<Small8, Deep8, Narrow8, LOAD_DIRECT>(plan, a, stream);
   if (spec.loader_b == LOAD_DIRECT_N)
-    return launch_grouped_type<Small16, Narrow16, LOAD_DIRECT_N>(plan, a, stream);
-  return launch_grouped_type<Small16, Narrow16, LOAD_DIRECT>(plan, a, stream);
+    return launch_grouped_type<Small16, Deep16, Narrow16, LOAD_DIRECT_N>(plan, a, stream);
+  return launch_grouped_type<Small16, Deep16, Narrow16, LOAD_DIRECT>(plan, a, stream);
 }
 
 #elif defined(G355_WGRAD)
@@ -1407,6 +1454,8 @@ hipError_t G355_WGRAD_LAUNCHER(G355_PART)(const GroupedPlan& plan, const LaunchS
                                           const GemmArgs& a, hipStream_t stream) {
   if (spec.loader_a == LOAD_GENERIC)
     return launch_grouped<Small16, LOAD_GENERIC, LOAD_GENERIC, false, MODE_WGRAD>(plan.grid, a, stream);
+  if (plan.grid <= kDeepGrid)
+    return launch_grouped<Deep16, LOAD_ROWS, LOAD_ROWS, false, MODE_WGRAD>(plan.grid, a, stream);
   return launch_grouped<Small16, LOAD_ROWS, LOAD_ROWS, false, MODE_WGRAD>(plan.grid, a, stream);
 }
 

@@ -32,22 +32,33 @@ int64_t most_row_tiles(int64_t G, int64_t T, int64_t bm) {
 }
 
 // Tile of a grouped product. A group of `avg` rows takes avg / bm full tiles
-// and on average half of one more. Full tiles of 256x256 sustain the highest
-// rate (the dense planner's figures); 64x128 tiles stream the weight with the
-// deepest ring, where a group hardly fills one tile and bytes decide.
-GroupedPlan plan_grouped(int64_t G, int64_t T, int64_t N, bool bytes1) {
+// and on average half of one more. The costs are microseconds per 128-byte K
+// slice of the slowest CU, from 180 shapes (2 to 32 groups of 32 to 400 rows,
+// N = 1024 and 4096, K = 2048 and 7168, the three types): one tile's slice
+// takes 0.65 us at 64x128 (deep ring), 0.72 at 128x128 (0.95 and 0.9 with B
+// read along its rows), 1.5 at 256x256; two 128x128 tiles on a CU 1.2. The
+// rule's choice is within 2% of the fastest on average. Examples, us at
+// 64x128 / 128x128 / 256x256: BF16, 32 groups of 400 rows, 4096 x 7168, 1715 /
+// 1040 / 824; 8 groups of 200, 4096 x 2048, 94 / 40 / 53; 8 groups of 32, 4096
+// x 7168, 76 / 126 / 149.
+GroupedPlan plan_grouped(int64_t G, int64_t T, int64_t N, bool b_rows) {
   const double groups = static_cast<double>(std::min(G, T));
   const double avg = static_cast<double>(T) / groups;
-  GroupedPlan best{128, 128, 0};
-  if (avg <= 64) {
-    best = {64, 128, 0};
-  } else {
-    const auto cost = [&](int b, int occupancy, double eff) {
-      const double wgs = groups * (avg / b + 0.5) * static_cast<double>(ceil_div(N, b));
-      return std::max(1.0, wgs / (kCUs * occupancy)) * b * b * occupancy / eff;
-    };
-    if (G <= kTableGroups && cost(256, 1, 0.85) < cost(128, 2, bytes1 ? 0.80 : 0.67)) best = {256, 256, 0};
-  }
+  const auto workgroups = [&](int bm, int bn) {
+    const double row_tiles = avg > 0.5 * bm ? avg / bm + 0.5 : 1.0;
+    return groups * row_tiles * static_cast<double>(ceil_div(N, bn));
+  };
+  // Rounds of the CUs' slots; a last, partial round costs more than its share.
+  const auto rounds = [](double wgs, double slots) {
+    return wgs <= slots ? 1.0 : wgs / slots + 0.2;
+  };
+  const double w128 = workgroups(128, 128);
+  const double c64 = rounds(workgroups(64, 128), kCUs) * (b_rows ? 0.95 : 0.65);
+  const double c128 = w128 <= kCUs ? (b_rows ? 0.9 : 0.72) : rounds(w128, 2 * kCUs) * 1.2;
+  const double c256 = G <= kTableGroups ? rounds(workgroups(256, 256), kCUs) * 1.5 : 1e30;
+  GroupedPlan best = c64 <= std::min(c128, c256) ? GroupedPlan{64, 128, 0}
+                     : c128 <= c256              ? GroupedPlan{128, 128, 0}
+                                                 : GroupedPlan{256, 256, 0};
   best.grid = most_row_tiles(G, T, best.bm) * ceil_div(N, best.bn);
   return best;
 }
@@ -114,7 +125,7 @@ gemm_status run_grouped(ElemType type, int64_t G, int64_t T, int64_t N, int64_t 
   if (!aligned(offsets, 4)) return GEMM_ERR_UNSUPPORTED;
 
   const int64_t es = bytes1 ? 1 : 2, ce = 16 / es;
-  GroupedPlan plan = plan_grouped(G, T, N, bytes1);
+  GroupedPlan plan = plan_grouped(G, T, N, !b_kmajor);
   LaunchSpec spec{};
   spec.fp8 = type == TY_FP8;
   spec.i8 = type == TY_I8;
