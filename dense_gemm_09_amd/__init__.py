@@ -155,7 +155,8 @@ def _need(t, nbytes: int, what: str):
         raise ValueError(f"{what} must be a device tensor")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous (pass the leading dimension instead)")
-    if _nbytes(t) < nbytes:
+    # The tensor's own bytes first: asking for its storage costs a microsecond.
+    if t.nbytes < nbytes and _nbytes(t) < nbytes:
         raise ValueError(f"{what} holds {_nbytes(t)} bytes, the call reads/writes {nbytes}")
 
 
@@ -176,8 +177,17 @@ def _check_operands(M, N, K, A, lda, la, B, ldb, lb, C, ldc, c_dtype, esize, bia
 def _stream(stream) -> int:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    # The raw handle: building torch's stream object costs more than a small launch.
+    global _current_stream
+    if _current_stream is None:
+        import torch
+        torch.cuda.init()
+        raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        _current_stream = lambda: raw(device())  # noqa: E731
+    return _current_stream()
+
+
+_current_stream = None
 
 
 def gemm_bf16(M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, beta, C, ldc, c_dtype,
