@@ -51,7 +51,7 @@ __device__ __forceinline__ int swz(int r) {
 }
 
 template <int BM_, int BN_, int WM_, int WN_, bool FP8_, int ROWB_, int STAGES_, int SPREAD_ = 1,
-          bool MX_ = false, bool I8_ = false>
+          bool MX_ = false, bool I8_ = false, int KG_ = 1>
 struct TileCfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ROWB = ROWB_, STAGES = STAGES_;
   // K-steps over which the global->LDS loads of one slice are issued.
@@ -68,8 +68,11 @@ struct TileCfg {
   // One FP32 scale per row of A and per column of B, applied in the epilogue.
   static constexpr bool SCALED = (FP8 && !MX) || I8;
   using Acc = std::conditional_t<I8, i32x16, f32x16>;
-  static constexpr int NWAVES = WM * WN;
-  static constexpr int NT = NWAVES * 64;
+  static constexpr int NWAVES = WM * WN;  // of one K group
+  // K groups: KG sets of NWAVES waves, each with a ring of its own, take the K
+  // slices in turn; their sums are added before the epilogue.
+  static constexpr int KG = KG_;
+  static constexpr int NT = NWAVES * KG * 64;
   static constexpr int ES = FP8 || I8 ? 1 : 2;  // bytes per element
   static constexpr int CPR = ROWB / 16;       // 16-byte chunks per row
   static constexpr int BKE = ROWB / ES;       // K elements per slice
@@ -89,7 +92,7 @@ struct TileCfg {
   static_assert(KSTEPS >= 1, "k steps");
   static_assert((BM / RPS) % NWAVES == 0 && (BN / RPS) % NWAVES == 0, "DMA segments per wave");
   static_assert(WTM % 32 == 0 && WTN % 32 == 0, "wave tile");
-  static_assert(STAGES >= 2 && STAGES * STAGE <= 160 * 1024, "LDS budget");
+  static_assert(STAGES >= 2 && KG * STAGES * STAGE <= 160 * 1024, "LDS budget");
   static_assert(SPREAD >= 1 && SPREAD <= KSTEPS, "load spread");
 };
 
@@ -674,14 +677,15 @@ __global__ void __launch_bounds__(C::NT)
 gemm_tile_kernel(GemmArgs p) {
   // The LDS block holds the ring of K slices, and after the main loop the
   // epilogue's staging strips.
-  constexpr int LDS_BYTES = C::STAGES * C::STAGE > EpiLayout<C>::TOTAL ? C::STAGES * C::STAGE
-                                                                       : EpiLayout<C>::TOTAL;
+  constexpr int RING = C::KG * C::STAGES * C::STAGE;
+  constexpr int LDS_BYTES = RING > EpiLayout<C>::TOTAL ? RING : EpiLayout<C>::TOTAL;
   static_assert(LDS_BYTES <= 160 * 1024, "LDS budget");
   __shared__ __attribute__((aligned(1024))) char smem[LDS_BYTES];
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kg = C::KG == 1 ? 0 : __builtin_amdgcn_readfirstlane((tid >> 6) / C::NWAVES);
+  const int wave = __builtin_amdgcn_readfirstlane((tid >> 6) - kg * C::NWAVES);
 
   // ---- which tile and which K range
   int tm, tn, split = 0;
@@ -728,7 +732,11 @@ gemm_tile_kernel(GemmArgs p) {
   const int m0 = tm * C::BM, n0 = tn * C::BN;
   const int k_begin = split * p.k_split_len;
   const int k_end = min(p.K, k_begin + p.k_split_len);
-  const int nk = k_end > k_begin ? (k_end - k_begin + C::BKE - 1) / C::BKE : 0;
+  // Slices in all, and of each K group (a group's last may lie past the end: zeros).
+  const int nk_all = k_end > k_begin ? (k_end - k_begin + C::BKE - 1) / C::BKE : 0;
+  const int nk = (nk_all + C::KG - 1) / C::KG;
+  // First K element of this group's slice s.
+  auto k_at = [&](int s) { return k_begin + (C::KG == 1 ? s : s * C::KG + kg) * C::BKE; };
 
   // ---- loaders
   // With 64-row tiles every byte of B is read by one workgroup only (each
@@ -790,8 +798,9 @@ gemm_tile_kernel(GemmArgs p) {
   // be in flight. Register-loaded slices are already in LDS by then.
   constexpr int DMA_BEHIND = DMA_PER_SLICE * (C::STAGES - 2);
 
-  auto a_tile = [&](int st) { return smem + st * C::STAGE; };
-  auto b_tile = [&](int st) { return smem + st * C::STAGE + C::A_BYTES; };
+  auto a_tile_of = [&](int g, int st) { return smem + (g * C::STAGES + st) * C::STAGE; };
+  auto a_tile = [&](int st) { return a_tile_of(kg, st); };
+  auto b_tile = [&](int st) { return a_tile(st) + C::A_BYTES; };
 
   auto fetch = [&](int st, int k0) __attribute__((always_inline)) {
     const bool full = k0 + C::BKE <= k_end;
@@ -825,7 +834,8 @@ gemm_tile_kernel(GemmArgs p) {
     constexpr int ROWS = RA + (LB == LOAD_DIRECT ? C::BN : 0);
     const int kc = k_end - k_end % C::CE;   // first element of the straddling chunk
     const int nb = (k_end - kc) * C::ES;    // its bytes below k_end: 1 .. 15
-    const int cl = (kc - (k_begin + (nk - 1) * C::BKE)) / C::CE;  // its chunk in the slice
+    const int cl = (kc - (k_begin + (nk_all - 1) * C::BKE)) / C::CE;  // its chunk in the slice
+    char* tail = a_tile_of((nk_all - 1) % C::KG, st);  // the group that has the slice
     // The thread index passes through an opaque move, so that none of the
     // per-lane address arithmetic below is hoisted out of the K loop (where
     // it would hold registers for the whole loop).
@@ -858,7 +868,7 @@ gemm_tile_kernel(GemmArgs p) {
         const int keep = nb - 4 * i;        // valid bytes of word i
         w[i] = keep >= 4 ? v : keep <= 0 ? 0u : (v & ((1u << (8 * keep)) - 1u));
       }
-      char* dst = (is_a ? a_tile(st) : b_tile(st)) + r * C::ROWB + ((cl ^ swz<C::CPR>(r)) << 4);
+      char* dst = tail + (is_a ? 0 : C::A_BYTES) + r * C::ROWB + ((cl ^ swz<C::CPR>(r)) << 4);
       *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -1064,7 +1074,7 @@ gemm_tile_kernel(GemmArgs p) {
   using Part3 = DmaPart<C, NA, NB, 3>;
   auto dma_part = [&](auto part, int s) {
     using Pt = decltype(part);
-    const int k0 = k_begin + s * C::BKE;
+    const int k0 = k_at(s);
     const int st = s % C::STAGES;
     if constexpr (LA == LOAD_ROWS)
       Pt::issue(ra, rb, a_tile(st), b_tile(st), wave, rsrc_a, rsrc_b, 0, 0, 0, k0, k_end, false);
@@ -1124,7 +1134,7 @@ gemm_tile_kernel(GemmArgs p) {
       if (ragged) patch_tail((j + 1) % C::STAGES);
     }
     if constexpr (ALL_DMA) dma_part(Part0{}, j + C::STAGES);
-    else fetch(j % C::STAGES, k_begin + (j + C::STAGES) * C::BKE);
+    else fetch(j % C::STAGES, k_at(j + C::STAGES));
   };
   auto step = [&](auto patch, int j, int t, const Frag (&ca)[C::FM], const Frag (&cb)[C::FN],
                   Frag (&na)[C::FM], Frag (&nb)[C::FN]) {
@@ -1158,7 +1168,7 @@ gemm_tile_kernel(GemmArgs p) {
     // slice 0 and the first k-step's fragments are read.
 #pragma unroll
     for (int s = 0; s < C::STAGES - 1; ++s) {
-      fetch(s, k_begin + s * C::BKE);
+      fetch(s, k_at(s));
       commit(s);
     }
     if constexpr (C::MX) mx_load(0);
@@ -1167,7 +1177,7 @@ gemm_tile_kernel(GemmArgs p) {
       if (ragged && nk == 1) patch_tail(0);
     }
     if constexpr (C::MX) mx_ready(0);
-    fetch(C::STAGES - 1, k_begin + (C::STAGES - 1) * C::BKE);
+    fetch(C::STAGES - 1, k_at(C::STAGES - 1));
     reads(0, 0, fa0, fb0);
     // Slices are taken U at a time so that each loop iteration holds an even
     // number of k-steps and the two fragment sets alternate statically. With
@@ -1210,6 +1220,32 @@ gemm_tile_kernel(GemmArgs p) {
   // it is in flight (the trailing zero-block loads included) and every wave is
   // done reading it.
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  if constexpr (C::KG == 2) {
+    // Group 1's sums pass through LDS, past the epilogue's staging area.
+    constexpr int PER_WAVE = C::FM * C::FN * 16 * 64;
+    static_assert(RING / 2 >= EpiLayout<C>::TOTAL && RING / 2 >= C::NWAVES * PER_WAVE * 4, "LDS");
+    float* sums = reinterpret_cast<float*>(smem + RING / 2) + wave * PER_WAVE + lane;
+    if (kg == 1) {
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sums[((i * C::FN + j) * 16 + e) * 64] = acc_bits(acc[i][j][e]);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (kg == 1) return;
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float x = sums[((i * C::FN + j) * 16 + e) * 64];
+          if constexpr (C::I8) acc[i][j][e] += __float_as_int(x);
+          else acc[i][j][e] += x;
+        }
+  }
   float* elds = reinterpret_cast<float*>(smem + wave * EpiLayout<C>::WAVE_BYTES);
   const int row0 = m0 + wm0, col0 = n0 + wn0;
   run_epilogue<C, OUT, SPLIT>(p, acc, elds, row0, col0, lane, split);
@@ -1383,18 +1419,18 @@ using Narrow16 = TileCfg<64, 128, 1, 2, false, 128, 6>;
 using Narrow8 = TileCfg<64, 128, 1, 2, true, 128, 6>;
 using Narrow8X = TileCfg<64, 128, 1, 2, true, 128, 6, 1, true>;
 // INT8: BF16's schedules (a slice is the same bytes and the same MFMAs).
-template <int BM, int BN, int WM, int WN, int STAGES, int SPREAD = 1>
-using CfgI8 = TileCfg<BM, BN, WM, WN, false, 128, STAGES, SPREAD, false, true>;
+template <int BM, int BN, int WM, int WN, int STAGES, int SPREAD = 1, int KG = 1>
+using CfgI8 = TileCfg<BM, BN, WM, WN, false, 128, STAGES, SPREAD, false, true, KG>;
 using BigI8 = CfgI8<256, 256, 2, 4, 2, 3>;
 using SmallI8 = CfgI8<128, 128, 2, 2, 2>;
 using ThinI8 = CfgI8<64, 256, 1, 4, 4>;
 using NarrowI8 = CfgI8<64, 128, 1, 2, 6>;
-// 128x128 with a ring of four slices (128 KB, one workgroup per CU), for
-// launches whose workgroups do not share a CU anyway: three slices in flight
-// instead of one.
-using Deep16 = TileCfg<128, 128, 2, 2, false, 128, 4>;
-using Deep8 = TileCfg<128, 128, 2, 2, true, 128, 4>;
-using DeepI8 = CfgI8<128, 128, 2, 2, 4>;
+// 128x128 with two K groups (128 KB, one workgroup per CU), for launches whose
+// workgroups do not share a CU anyway: two waves on every SIMD, and twice the
+// copies in flight.
+using Deep16 = TileCfg<128, 128, 2, 2, false, 128, 2, 1, false, false, 2>;
+using Deep8 = TileCfg<128, 128, 2, 2, true, 128, 2, 1, false, false, 2>;
+using DeepI8 = CfgI8<128, 128, 2, 2, 2, 1, 2>;
 constexpr int64_t kDeepGrid = 256;
 
 #if defined(G355_I8)
