@@ -476,7 +476,11 @@ def _workspace(M, N, K, fp8, workspace, workspace_bytes, stream):
         import torch
         # Allocated on the stream the kernels run on: torch's caching allocator
         # then gives the block to a later allocation only in that stream's
-        # order, i.e. after this call's kernels have finished with it.
+        # order, i.e. after this call's kernels have finished with it. (Without a
+        # stream argument that is the current one, and no context is entered:
+        # that costs more than a small launch.)
+        if stream is None:
+            return torch.empty(need, dtype=torch.uint8, device="cuda"), need
         s = _torch_stream(stream)
         with torch.cuda.stream(s):
             workspace = torch.empty(need, dtype=torch.uint8, device=s.device)
