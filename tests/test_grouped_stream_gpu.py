@@ -143,6 +143,19 @@ def test_weight_gradient(N, K, G, out):
         check_exact(c[i].float().cpu().numpy(), y.numpy(), f"group {i}")
 
 
+def test_k_zero_and_no_rows():
+    """K = 0 leaves act(beta C + bias); a weight gradient over no rows is zero."""
+    G, N, T, off = len(SIZES), 4096, sum(SIZES), offsets(SIZES)
+    c = torch.full((T, N), 2.0, device="cuda")
+    b = ints((G, N), 5, 3)
+    g.gemm_grouped_bf16(G, T, N, 0, 1.0, None, 1, dev(off), None, 1, COL, 0, -1.0, c, N, OUT_F32, dev(bits(b)), ACT_RELU)
+    check_exact(c.cpu().numpy(), np.maximum(b[np.repeat(np.arange(G), SIZES)] - 2, 0), "K = 0")
+    dw = torch.full((3, 2048, 4096), float("nan"), device="cuda")
+    g.gemm_grouped_bf16_wgrad(3, 0, 2048, 4096, 1.0, None, 2048, None, 4096, dev(offsets([0, 0, 0])), 0.0, dw, 4096,
+                              2048 * 4096, OUT_F32)
+    assert torch.all(dw == 0).item()
+
+
 def test_a_nan_stays_in_its_own_rows_and_its_own_expert():
     """A NaN token spoils its row alone, a NaN weight its group alone, an infinite row of no group nothing."""
     G, N, K, T, off = len(SIZES), 3900, 64, sum(SIZES) + 5, offsets(SIZES)
