@@ -1425,6 +1425,11 @@ using BigI8 = CfgI8<256, 256, 2, 4, 2, 3>;
 using SmallI8 = CfgI8<128, 128, 2, 2, 2>;
 using ThinI8 = CfgI8<64, 256, 1, 4, 4>;
 using NarrowI8 = CfgI8<64, 128, 1, 2, 6>;
+// 64x128 with three slices (72 KB): two workgroups per CU, so that one's start
+// and end (a group's product has few slices) overlap the other's loads.
+using Pair16 = TileCfg<64, 128, 1, 2, false, 128, 3>;
+using Pair8 = TileCfg<64, 128, 1, 2, true, 128, 3>;
+using PairI8 = CfgI8<64, 128, 1, 2, 3>;
 // 128x128 with two K groups (128 KB, one workgroup per CU), for launches whose
 // workgroups do not share a CU anyway: two waves on every SIMD, and twice the
 // copies in flight.
@@ -1455,11 +1460,13 @@ hipError_t G355_I8_LAUNCHER(G355_RAGGED, G355_PART)(const Plan& plan, const Laun
 #elif defined(G355_GROUPED)
 
 // One element type's tiles: 128x128 (with a deep ring where a CU has one workgroup), and 64x128.
-template <class SMALL, class DEEP, class NARROW, int LB>
+template <class SMALL, class DEEP, class NARROW, class PAIR, int LB>
 static hipError_t launch_grouped_type(const GroupedPlan& plan, const GemmArgs& a,
                                       hipStream_t stream) {
   constexpr bool R = G355_RAGGED != 0;
-  if (plan.bm == 64) return launch_grouped<NARROW, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
+  if (plan.bm == 64)
+    return plan.grid <= kDeepGrid ? launch_grouped<NARROW, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream)
+                                  : launch_grouped<PAIR, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
   if (plan.grid <= kDeepGrid) return launch_grouped<DEEP, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
   return launch_grouped<SMALL, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
 }
@@ -1477,11 +1484,11 @@ hipError_t G355_GROUPED_LAUNCHER(G355_RAGGED, G355_PART)(const GroupedPlan& plan
     else
       return launch_grouped<Small16, LOAD_GENERIC, LOAD_GENERIC, false, MODE_GROUPED>(plan.grid, a, stream);
   }
-  if (spec.i8) return launch_grouped_type<SmallI8, DeepI8, NarrowI8, LOAD_DIRECT>(plan, a, stream);
-  if (spec.fp8) return launch_grouped_type<Small8, Deep8, Narrow8, LOAD_DIRECT>(plan, a, stream);
+  if (spec.i8) return launch_grouped_type<SmallI8, DeepI8, NarrowI8, PairI8, LOAD_DIRECT>(plan, a, stream);
+  if (spec.fp8) return launch_grouped_type<Small8, Deep8, Narrow8, Pair8, LOAD_DIRECT>(plan, a, stream);
   if (spec.loader_b == LOAD_DIRECT_N)
-    return launch_grouped_type<Small16, Deep16, Narrow16, LOAD_DIRECT_N>(plan, a, stream);
-  return launch_grouped_type<Small16, Deep16, Narrow16, LOAD_DIRECT>(plan, a, stream);
+    return launch_grouped_type<Small16, Deep16, Narrow16, Pair16, LOAD_DIRECT_N>(plan, a, stream);
+  return launch_grouped_type<Small16, Deep16, Narrow16, Pair16, LOAD_DIRECT>(plan, a, stream);
 }
 
 #elif defined(G355_WGRAD)

@@ -20,13 +20,23 @@
 //   turn t+2 on: at most 2 copies a turn, each with five turns to arrive. Copies
 //   complete in order, so a fixed count (vmcnt 10) is all that a turn waits for.
 // * 16x16 MFMAs (32 BF16, 64 INT8 or 128 FP8 elements of K). The same loop with
-//   the 32x32 shapes of the tile kernel ran 1316 instead of 1191 us (16384 x
-//   14336 x 4096, BF16) and 696 instead of 620 us (INT8).
+//   the 32x32 shapes of the tile kernel, epilogue left out, ran 1316 instead of
+//   1191 us (16384 x 14336 x 4096, BF16) and 696 instead of 620 us (INT8).
 // * C is computed transposed (B's fragment first): a lane then holds 4
-//   consecutive columns of one row per MFMA block. The epilogue works on
-//   registers and stores 16 bytes per lane, 64 contiguous bytes per row,
-//   without LDS; for BF16 outputs, neighbouring lane groups swap halves of two
-//   blocks first.
+//   consecutive columns of one row per MFMA block, and the order of B's rows in
+//   a fragment makes that 8 for BF16 outputs. The epilogue works on registers
+//   and stores 16 bytes per lane, 64 contiguous bytes per row, without LDS. The
+//   stores go through the caches, which join the halves of a line: non-temporal
+//   ones of this shape reach 2.4-2.8 TB/s, these 5.0 (a fill kernel 6.9).
+// * A workgroup per CU takes its tiles as one stream: copies for the next tile
+//   are in flight while this one's epilogue runs (8 experts' forward pass, no
+//   activation, 1602 -> 1543 us; short products lose nothing).
+//
+// Measured, all three at 16384 rows over 8 experts, 14336 x 4096: forward with bias
+// and GELU 1560 us (1230 TFLOP/s), the same without them 1380 us, weight gradient
+// in FP32 1700 us. The matrix cores are busy 64% of the cycles and the card runs
+// at its power limit, at 1.65 GHz; GELU is vector arithmetic that nothing
+// overlaps (120 us), stores and their acknowledgement cost 6 us a tile.
 //
 // Operands that are contiguous along the other axis (the weight of an input
 // gradient, both operands of a weight gradient) are copied as they lie: LDS
@@ -51,7 +61,6 @@ typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 // Global vectors at any element alignment (the hardware takes them).
 typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
-typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
 typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
 
 template <int TY_, int OUT_, bool AR_, bool BR_, int MODE_>
@@ -62,21 +71,33 @@ struct TurnCfg {
   static constexpr int BKE = 128 / ES;       // K elements per slice
   static constexpr int CE = 16 / ES;         // K elements per 16-byte chunk
   static_assert(TY == TY_BF16 || (!AR && !BR), "rows of one byte: K-major only");
+  // BF16 outputs: column 8q + 4u + e of a 32-column half is element e of lane
+  // group q of MFMA block u; FP32: column 16u + 4q + e.
+  static constexpr bool PAIR = OUT == OUT_BF16;
   using Acc = std::conditional_t<TY == TY_I8, i32x4, f32x4>;
 };
 
 // Chunk c of row r of a K-major tile is stored at c ^ turn_swizzle(r). A
 // fragment read takes chunks c and c ^ 1 of 16 rows in its lanes 0-31 (others in
-// 32-63); the LDS serves lanes 0-3, 12-15 and 20-27 of them at once, then the
-// rest. Both sets touch 16 distinct 16-byte slots of the 64 banks. (With the
-// tile kernel's swizzle, made for 32 rows of one chunk, half of the LDS cycles of
-// these reads were conflicts.)
-__device__ __forceinline__ int turn_swizzle(int r) { return (r >> 1) & 7; }
+// 32-63): consecutive rows, or (PAIRED) those that differ in bits 0, 1, 3 and 4.
+// The LDS serves lanes 0-3, 12-15 and 20-27 of them at once, then the rest: both
+// sets touch 16 distinct 16-byte slots of the 64 banks. (With the tile kernel's
+// swizzle, made for 32 rows of one chunk, half of the LDS cycles of these reads
+// were conflicts; the counter now reads 0.)
+template <bool PAIRED>
+__device__ __forceinline__ int turn_swizzle(int r) {
+  if constexpr (PAIRED) return ((r >> 1) & 1) | ((r >> 2) & 6);
+  else return (r >> 1) & 7;
+}
 
 // Chunk c of row k of an operand copied as rows of 128 columns (256 bytes) is
-// stored at c ^ rows_swizzle(k): the 32-byte pieces that a transposing read takes
-// of eight rows then lie on different banks.
-__device__ __forceinline__ int rows_swizzle(int k) { return 2 * (k & 3) + 8 * ((k >> 3) & 1); }
+// stored at c ^ rows_swizzle(k): the four rows of a transposing read, whose
+// pieces span 32 bytes (or 64, PAIRED), then lie on different banks.
+template <bool PAIRED>
+__device__ __forceinline__ int rows_swizzle(int k) {
+  if constexpr (PAIRED) return 4 * (k & 3);
+  else return 2 * (k & 3) + 8 * ((k >> 3) & 1);
+}
 
 // ------------------------------------------------------------------------ copies
 
@@ -85,7 +106,7 @@ __device__ __forceinline__ int rows_swizzle(int k) { return 2 * (k & 3) + 8 * ((
 // (their results are never stored); chunks that do not end by K read zeros:
 // they get an offset past the descriptor's range. Offsets are from the tile's
 // first row, 32 bits (the host checks 256 rows).
-template <class C>
+template <class C, bool PAIRED>
 struct KMajorCopy {
   uint32_t off[2][2];
   int last[2];  // K element after the lane's chunk, slice-relative
@@ -99,7 +120,7 @@ struct KMajorCopy {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int r = 16 * wave + 8 * q + (lane >> 3);
-      const int c = (lane & 7) ^ turn_swizzle(r);
+      const int c = (lane & 7) ^ turn_swizzle<PAIRED>(r);
       last[q] = c * C::CE + C::CE;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -124,7 +145,7 @@ struct KMajorCopy {
 // stored. The range check drops a 4-byte word that lies partly past the range,
 // which for an odd column count holds the last element: the range is 2 bytes
 // longer (the host makes sure that those stay on the operand's last page).
-template <class C>
+template <class C, bool PAIRED>
 struct RowsCopy {
   uint32_t off[2][2];
   const char* base;  // of the slice
@@ -139,7 +160,7 @@ struct RowsCopy {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int k = 8 * wave + 4 * q + (lane >> 4);
-      const int c = (lane & 15) ^ rows_swizzle(k);
+      const int c = (lane & 15) ^ rows_swizzle<PAIRED>(k);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int n = 128 * h + 8 * c;
@@ -166,29 +187,30 @@ __device__ __forceinline__ i32x4 low(const i32x8& x) { return __builtin_shufflev
 __device__ __forceinline__ i32x4 high(const i32x8& x) { return __builtin_shufflevector(x, x, 4, 5, 6, 7); }
 // Fragments of one operand: NB blocks of 16 rows (columns of C) per half, two
 // 16-byte pieces each (64 bytes of K a piece over the four lane groups).
-template <int NB, bool ROWS>
+template <class C, int NB, bool ROWS, bool PAIRED>
 struct Fragments {
-  // ROWS: the swizzle reaches the bits that tell blocks apart, so every block
-  // has an address of its own.
-  static constexpr int NA = ROWS ? NB : 2;
+  // ROWS, not PAIRED: the swizzle reaches the bits that tell blocks apart, so
+  // every block has an address of its own.
+  static constexpr int NA = ROWS ? (PAIRED ? 1 : NB) : 2;
   int addr[NA];
 
   // row0: the wave's first row in a half (a multiple of 16 * NB).
   __device__ __forceinline__ void init(int base, int row0, int lane) {
     const int d = lane & 15, g = lane >> 4;
     if constexpr (!ROWS) {
-      const int r = row0 + d;  // of block 0
+      // Row d of block b: 16 b + d, or PAIRED 8 (d / 4) + 4 b + d % 4.
+      const int r = row0 + (PAIRED ? 8 * (d >> 2) + (d & 3) : d);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
-        addr[t] = base + r * 128 + (((4 * t + g) ^ turn_swizzle(r)) << 4);
+        addr[t] = base + r * 128 + (((4 * t + g) ^ turn_swizzle<PAIRED>(r)) << 4);
     } else {
       // Lane d of a group points at row d / 4 of four and at 4 columns of it;
-      // it receives column d of the four rows.
+      // it receives column d (PAIRED: 8 (d / 4) + 4 b + d % 4) of the four rows.
       const int k = 8 * g + (d >> 2);
 #pragma unroll
       for (int b = 0; b < NA; ++b) {
-        const int c = ((row0 + 16 * b) >> 3) + ((d & 3) >> 1);
-        addr[b] = base + k * 256 + ((c ^ rows_swizzle(k)) << 4) + 8 * (d & 1);
+        const int c = PAIRED ? (row0 >> 3) + (d & 3) : ((row0 + 16 * b) >> 3) + ((d & 3) >> 1);
+        addr[b] = base + k * 256 + ((c ^ rows_swizzle<PAIRED>(k)) << 4) + (PAIRED ? 0 : 8 * (d & 1));
       }
     }
   }
@@ -204,25 +226,27 @@ struct Fragments {
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-          v[b][t] = *reinterpret_cast<G355_LDS const i32x4*>(addr[t] + AT + b * 16 * 128);
+          v[b][t] = *reinterpret_cast<G355_LDS const i32x4*>(addr[t] + AT + b * (PAIRED ? 4 : 16) * 128);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
         f[b] = __builtin_shufflevector(v[b][0], v[b][1], 0, 1, 2, 3, 4, 5, 6, 7);
     } else {
       i32x2 v[NB][4];
+      constexpr int P = PAIRED ? 8 : 0;  // bytes from one block to the next
       if constexpr (NB == 2) {
         asm volatile(
             "ds_read_b64_tr_b16 %0, %8 offset:%10\n\tds_read_b64_tr_b16 %1, %8 offset:%11\n\t"
-            "ds_read_b64_tr_b16 %4, %9 offset:%10\n\tds_read_b64_tr_b16 %5, %9 offset:%11\n\t"
+            "ds_read_b64_tr_b16 %4, %9 offset:%14\n\tds_read_b64_tr_b16 %5, %9 offset:%15\n\t"
             "ds_read_b64_tr_b16 %2, %8 offset:%12\n\tds_read_b64_tr_b16 %3, %8 offset:%13\n\t"
-            "ds_read_b64_tr_b16 %6, %9 offset:%12\n\tds_read_b64_tr_b16 %7, %9 offset:%13\n\t"
+            "ds_read_b64_tr_b16 %6, %9 offset:%16\n\tds_read_b64_tr_b16 %7, %9 offset:%17\n\t"
             "s_waitcnt lgkmcnt(0)"
             : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[0][2]), "=&v"(v[0][3]), "=&v"(v[1][0]),
               "=&v"(v[1][1]), "=&v"(v[1][2]), "=&v"(v[1][3])
-            : "v"(addr[0]), "v"(addr[NA - 1]), "n"(AT), "n"(AT + 1024), "n"(AT + 8192), "n"(AT + 9216)
+            : "v"(addr[0]), "v"(addr[NA - 1]), "n"(AT), "n"(AT + 1024), "n"(AT + 8192), "n"(AT + 9216),
+              "n"(AT + P), "n"(AT + P + 1024), "n"(AT + P + 8192), "n"(AT + P + 9216)
             : "memory");
       } else {
-        static_assert(NB == 4, "A's blocks");
+        static_assert(NB == 4 && !PAIRED, "A's blocks");
         asm volatile(
             "ds_read_b64_tr_b16 %0, %16 offset:%20\n\tds_read_b64_tr_b16 %1, %16 offset:%21\n\t"
             "ds_read_b64_tr_b16 %4, %17 offset:%20\n\tds_read_b64_tr_b16 %5, %17 offset:%21\n\t"
@@ -275,27 +299,30 @@ struct TileVectors {
 };
 
 // C = act(alpha * scale_a[m] * scale_b[n] * acc + beta * C + bias[n]) from the
-// registers. Lane l of block (i, j) holds row 16 i + l % 16 and the columns
-// 16 j + 4 (l / 16) + 0..3 (in their halves). c: the tile's first element; row0,
-// col0: the wave's first row and column in it. WHOLE: every column exists. ACT:
-// the activation, or -1: p.act.
+// registers. Lane l of block (i, j) holds row 16 i + l % 16 (in its half) and
+// the columns of TurnCfg::PAIR. c: the tile's first element; row0, col0: the
+// wave's first row and column in it. WHOLE: every column exists. ACT: the
+// activation, or -1: p.act.
 template <class C, int ACT, bool ZERO, bool WHOLE>
 __device__ __forceinline__ void turn_epilogue(const GemmArgs& p, const typename C::Acc (&acc)[8][4],
                                               const TileVectors& tv, char* c, int rows, int cols,
                                               int row0, int col0, int lane) {
   constexpr bool SCALED = C::ES == 1;
+  constexpr int W = C::PAIR ? 8 : 4;   // consecutive columns per store
+  constexpr int RUNS = 8 / W;          // of a half
   constexpr int OB = C::OUT == OUT_F32 ? 4 : 2;
   const int q = lane >> 4, r = lane & 15;
-  // Two blocks (one half of the wave's columns) at a time, rows inside: only
-  // their columns' vectors are in registers.
+  // Half by half, rows inside: the columns' vectors of one half are in registers.
+  // A row's two runs of FP32 fill a 128-byte line one after the other (13
+  // gradients of 3200 x 11136: 548 us with the rows between them, 378 so).
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int n0 = col0 + 128 * h + 4 * q;  // block u: n0 + 16 u + 0..3
+    const int n0 = col0 + 128 * h + W * q;  // run s: n0 + 16 s
     float cs[8], bias[8];
     int zb[8];
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
-      const int n = n0 + 16 * (x >> 2) + (x & 3);
+      const int n = n0 + 16 * (x / W) + x % W;
       cs[x] = p.alpha;
       if constexpr (SCALED) cs[x] = p.alpha * tv.scale_b[n];
       bias[x] = C::MODE != MODE_WGRAD && p.bias ? tv.bias[n] : 0.f;
@@ -303,73 +330,62 @@ __device__ __forceinline__ void turn_epilogue(const GemmArgs& p, const typename 
       if (ZERO) zb[x] = tv.sum_b[n];
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      __builtin_amdgcn_sched_barrier(0);  // one row block's registers at a time
-      if (row0 + 128 * (i >> 2) + 16 * (i & 3) >= rows) continue;
+    for (int is = 0; is < 8 * RUNS; ++is) {
+      const int i = is / RUNS, s = is % RUNS;
+      __builtin_amdgcn_sched_barrier(0);  // one run's registers at a time
+      const int n = n0 + 16 * s;
       const int m = row0 + 128 * (i >> 2) + 16 * (i & 3) + r;
-      const bool row_ok = m < rows;
+      if (m >= rows || (!WHOLE && n >= cols)) continue;
+      const bool vec = WHOLE || n + W <= cols;
       float sa = 1.f;
       int za = 0;
       if constexpr (SCALED) sa = tv.scale_a[m];
       if (ZERO) za = tv.zero_a[m];
-      char* row = c + m * p.ldc * OB;
-      float v[8];
+      char* at = c + m * p.ldc * OB + n * OB;
+      float v[W];
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const auto a = acc[i][2 * h + (x >> 2)][x & 3];
+      for (int e = 0; e < W; ++e) {
+        const auto a = acc[i][2 * h + (C::PAIR ? e >> 2 : s)][e & 3];
         float z;
-        if constexpr (C::TY == TY_I8) z = i8_sum(a, ZERO, za, static_cast<double>(zb[x]));
+        if constexpr (C::TY == TY_I8) z = i8_sum(a, ZERO, za, static_cast<double>(zb[W * s + e]));
         else z = a;
-        v[x] = fmaf(z, SCALED ? sa * cs[x] : cs[x], bias[x]);
+        v[e] = fmaf(z, SCALED ? sa * cs[W * s + e] : cs[W * s + e], bias[W * s + e]);
       }
-      if (p.beta != 0.f && row_ok) {
+      if (p.beta != 0.f) {
+        float in[W];
+        if (vec) {
+          if constexpr (C::OUT == OUT_BF16) {
+            const u32x4 h = *reinterpret_cast<const u32x4_at2*>(at);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int n = n0 + 16 * u;
-          float in[4] = {0.f, 0.f, 0.f, 0.f};
-          if (WHOLE || n + 4 <= cols) {
-            if constexpr (C::OUT == OUT_BF16) {
-              const u32x2 b = *reinterpret_cast<const u32x2_at2*>(row + n * OB);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                in[e] = __uint_as_float(e & 1 ? b[e >> 1] & 0xffff0000u : b[e >> 1] << 16);
-            } else {
-              const f32x4 b = *reinterpret_cast<const f32x4_at4*>(row + n * OB);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) in[e] = b[e];
-            }
+            for (int e = 0; e < W; ++e)
+              in[e] = __uint_as_float(e & 1 ? h[e >> 1] & 0xffff0000u : h[e >> 1] << 16);
           } else {
+            const f32x4 h = *reinterpret_cast<const f32x4_at4*>(at);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (n + e < cols) in[e] = load_cin1<C::OUT>(row, n + e);
+            for (int e = 0; e < W; ++e) in[e] = h[e];
           }
+        } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[4 * u + e] = fmaf(p.beta, in[e], v[4 * u + e]);
+          for (int e = 0; e < W; ++e) in[e] = n + e < cols ? load_cin1<C::OUT>(at, e) : 0.f;
         }
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[e] = fmaf(p.beta, in[e], v[e]);
       }
 #pragma unroll
-      for (int x = 0; x < 8; ++x) v[x] = apply_act<C::OUT>(v[x], ACT < 0 ? p.act : ACT);
-      if constexpr (WHOLE && C::OUT == OUT_BF16) {
-        // Lane groups 2x and 2x + 1 swap: the even one then holds columns
-        // 8x .. 8x + 7 of block 0, the odd one those of block 1.
-        const auto x = __builtin_amdgcn_permlane16_swap(f32x2_to_bf16x2_bits(v[0], v[1]),
-                                                        f32x2_to_bf16x2_bits(v[4], v[5]), false, false);
-        const auto y = __builtin_amdgcn_permlane16_swap(f32x2_to_bf16x2_bits(v[2], v[3]),
-                                                        f32x2_to_bf16x2_bits(v[6], v[7]), false, false);
-        const int n = col0 + 128 * h + 16 * (q & 1) + 8 * (q >> 1);
-        if (row_ok) *reinterpret_cast<u32x4_at2*>(row + n * OB) = u32x4{x[0], y[0], x[1], y[1]};
-      } else if (row_ok) {
+      for (int e = 0; e < W; ++e) v[e] = apply_act<C::OUT>(v[e], ACT < 0 ? p.act : ACT);
+      if (vec) {
+        if constexpr (C::OUT == OUT_BF16) {
+          u32x4 h;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int n = n0 + 16 * u;
-          if (C::OUT == OUT_F32 && (WHOLE || n + 4 <= cols)) {
-            *reinterpret_cast<f32x4_at4*>(row + n * OB) = f32x4{v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]};
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (n + e < cols) store_out1<C::OUT>(row, n + e, v[4 * u + e], 1.f, 0.f);
-          }
+          for (int e = 0; e < 4; ++e) h[e] = f32x2_to_bf16x2_bits(v[2 * e], v[2 * e + 1]);
+          *reinterpret_cast<u32x4_at2*>(at) = h;
+        } else {
+          *reinterpret_cast<f32x4_at4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
         }
+      } else {
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+          if (n + e < cols) store_out1<C::OUT>(at, e, v[e], 1.f, 0.f);
       }
     }
   }
@@ -515,10 +531,10 @@ __global__ void __launch_bounds__(kTurnThreads, 2) gemm_turn_kernel(GemmArgs p) 
   bool more = turn_tile<C>(p, sh, nwg, v, lane, cur);
   if (!more) return;
 
-  std::conditional_t<C::AR, RowsCopy<C>, KMajorCopy<C>> ca;
-  std::conditional_t<C::BR, RowsCopy<C>, KMajorCopy<C>> cb;
-  Fragments<4, C::AR> ra;
-  Fragments<2, C::BR> rb;
+  std::conditional_t<C::AR, RowsCopy<C, false>, KMajorCopy<C, false>> ca;
+  std::conditional_t<C::BR, RowsCopy<C, C::PAIR>, KMajorCopy<C, C::PAIR>> cb;
+  Fragments<C, 4, C::AR, false> ra;
+  Fragments<C, 2, C::BR, C::PAIR> rb;
 
   // The copies' place in the stream: K0 of their slice, and what is left of their tile.
   int ck0 = 0, cK = 0, cleft = 0;
@@ -719,11 +735,11 @@ __global__ void __launch_bounds__(kTurnThreads, 2) gemm_turn_kernel(GemmArgs p) 
         for (int i = 0; i < 4; ++i) x[i] = l < 16 ? x[i] : 0;
         return __builtin_shufflevector(x, i32x4{0, 0, 0, 0}, 0, 1, 2, 3, 4, 5, 6, 7);
       };
-      const int rowb = 256 + 32 * (wave & 3) + d16;
+      const int rowb = 256 + 32 * (wave & 3) + (C::PAIR ? 8 * (d16 >> 2) + (d16 & 3) : d16);
       // (The fragments in registers belong to the next tile.)
       i32x8 y[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = chunk(rowb + 128 * (j >> 1) + 16 * (j & 1));
+      for (int j = 0; j < 4; ++j) y[j] = chunk(rowb + 128 * (j >> 1) + (C::PAIR ? 4 : 16) * (j & 1));
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const i32x8 x = chunk(64 * (wave >> 2) + 128 * (i >> 2) + 16 * (i & 3) + d16);

@@ -36,11 +36,11 @@ int64_t most_row_tiles(int64_t G, int64_t T, int64_t bm) {
 // slice of the slowest CU, from 180 shapes (2 to 32 groups of 32 to 400 rows,
 // N = 1024 and 4096, K = 2048 and 7168, the three types): one tile's slice
 // takes 0.65 us at 64x128 (deep ring), 0.72 at 128x128 (0.95 and 0.9 with B
-// read along its rows), 1.5 at 256x256; two 128x128 tiles on a CU 1.2. The
-// rule's choice is within 2% of the fastest on average. Examples, us at
-// 64x128 / 128x128 / 256x256: BF16, 32 groups of 400 rows, 4096 x 7168, 1715 /
-// 1040 / 824; 8 groups of 200, 4096 x 2048, 94 / 40 / 53; 8 groups of 32, 4096
-// x 7168, 76 / 126 / 149.
+// read along its rows), 1.5 at 256x256; two 128x128 tiles on a CU 1.2, two
+// 64x128 tiles 1.05 (1.3). Examples, us at 64x128 / 128x128 / 256x256: BF16, 32
+// groups of 400 rows, 4096 x 7168, 1715 / 1040 / 824; 8 groups of 200, 4096 x
+// 2048, 94 / 40 / 53; 24 groups of a row or two, 2048 x 4096, 64.8 / 78.3; INT8,
+// 30 groups of 4 rows, 4096 x 2048, 47 / 55, of 50 rows 63 / 60.
 GroupedPlan plan_grouped(int64_t G, int64_t T, int64_t N, bool b_rows) {
   const double groups = static_cast<double>(std::min(G, T));
   const double avg = static_cast<double>(T) / groups;
@@ -53,7 +53,8 @@ GroupedPlan plan_grouped(int64_t G, int64_t T, int64_t N, bool b_rows) {
     return wgs <= slots ? 1.0 : wgs / slots + 0.2;
   };
   const double w128 = workgroups(128, 128);
-  const double c64 = rounds(workgroups(64, 128), kCUs) * (b_rows ? 0.95 : 0.65);
+  const double w64 = workgroups(64, 128);
+  const double c64 = w64 <= kCUs ? (b_rows ? 0.95 : 0.65) : rounds(w64, 2 * kCUs) * (b_rows ? 1.3 : 1.05);
   const double c128 = w128 <= kCUs ? (b_rows ? 0.9 : 0.72) : rounds(w128, 2 * kCUs) * 1.2;
   const double c256 = G <= kTableGroups ? rounds(workgroups(256, 256), kCUs) * 1.5 : 1e30;
   GroupedPlan best = c64 <= std::min(c128, c256) ? GroupedPlan{64, 128, 0}
