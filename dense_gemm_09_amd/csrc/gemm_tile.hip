@@ -1432,7 +1432,7 @@ using Pair8 = TileCfg<64, 128, 1, 2, true, 128, 3>;
 using PairI8 = CfgI8<64, 128, 1, 2, 3>;
 // 128x128 with two K groups (128 KB, one workgroup per CU), for launches whose
 // workgroups do not share a CU anyway: two waves on every SIMD, and twice the
-// copies in flight.
+// copies in flight (INT8 1024 x 4096 x 4096: 27 us, with one group 35).
 using Deep16 = TileCfg<128, 128, 2, 2, false, 128, 2, 1, false, false, 2>;
 using Deep8 = TileCfg<128, 128, 2, 2, true, 128, 2, 1, false, false, 2>;
 using DeepI8 = CfgI8<128, 128, 2, 2, 2, 1, 2>;

