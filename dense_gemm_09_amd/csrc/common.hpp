@@ -61,14 +61,6 @@ struct GemmArgs {
   int64_t stride_b;       // elements from one group's B (weight gradient: C) to the next
 };
 
-// Groups that gemm_turn.hip's table of them holds (a multiple of 64).
-constexpr int kTableGroups = 1024;
-
-// Tiles per group from which the weight gradient deals each group's tiles to
-// the XCDs in eighths (below, workgroups go round robin: an eighth of fewer
-// tiles than this shares little).
-constexpr int kWgradXcdTiles = 64;
-
 // ---------------------------------------------------------------- conversions
 
 __device__ __forceinline__ float bf16_bits_to_f32(uint16_t h) {

@@ -40,6 +40,7 @@
 #include "common.hpp"
 #include "grouping.hpp"
 #include "internal.hpp"
+#include "row_copies.hpp"
 
 namespace g355 {
 
@@ -223,15 +224,10 @@ struct NmajorLoader {
 // Either operand of the weight gradient: the contraction runs over rows of
 // memory (tokens), COLS consecutive columns of which make a tile, BF16. Slices
 // land in the N-major LDS tile of NmajorLoader and are read by the same
-// transposing reads. Unlike there, rows may start at any 2-byte boundary and
-// the operand may be of any size: the descriptor's base moves with the slice
-// (64-bit scalar arithmetic), so a lane's offset stays below 64 rows, and its
-// range ends with the last row of the K range, so that rows past it read
-// zeros. A chunk that straddles the last column reads what follows the row
-// into columns that are never stored. The range check drops a 4-byte word
-// that lies partly past the range, which for an odd column count is the word
-// of the last element itself: the range is therefore 2 bytes longer (the
-// caller makes sure that those stay on the operand's last page).
+// transposing reads. Unlike there, the operand may be of any size: the
+// descriptor's base moves with the slice (64-bit scalar arithmetic), so a lane's
+// offset stays below 64 rows, and its range ends with the last row of the K
+// range (row_copies.hpp).
 template <class C, int COLS, int NW = C::NWAVES>
 struct RowsLoader {
   static constexpr int ROWN = COLS * 2;
@@ -239,7 +235,7 @@ struct RowsLoader {
   static constexpr int RPSN = 1024 / ROWN;
   static constexpr int SEGS = C::BKE / RPSN;
   static constexpr int IPW = SEGS / NW;
-  static constexpr uint32_t kNowhere = 0x80000000u;  // past every range
+  static_assert(C::ES == 1 || C::BKE <= kSliceRows, "rows_range");
   uint32_t off[IPW];
   const char* base;
   int64_t ld2;  // bytes per row
@@ -254,8 +250,7 @@ struct RowsLoader {
     for (int i = 0; i < IPW; ++i) {
       const int r = (wave * IPW + i) * RPSN + lane / CPRN;
       const int lc = (lane % CPRN) ^ (4 * (r & 3));
-      const int n = col0 + 8 * lc;
-      off[i] = n < cols ? static_cast<uint32_t>(r * ld2 + n * 2) : kNowhere;
+      off[i] = rows_offset(r, ld2, col0 + 8 * lc, cols);
     }
   }
 
@@ -264,11 +259,8 @@ struct RowsLoader {
                                             int koff, uint32_t oob, int k0, int k_end,
                                             bool full) const {
     (void)koff, (void)oob, (void)full;
-    const int rem = k_end - k0;
-    const int64_t want = rem > 0 ? (rem - 1) * ld2 + cols * 2 + 2 : 0;
-    const int range = static_cast<int>(want < INT32_MAX ? want : INT32_MAX);
     const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(base + k0 * ld2), 0, range, kBufferWord3);
+        const_cast<char*>(base + k0 * ld2), 0, rows_range(k_end - k0, static_cast<uint32_t>(ld2), cols), kBufferWord3);
 #pragma unroll
     for (int i = I0; i < I1; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (G355_LDS void*)(lds_tile + (wave * IPW + i) * 1024),

@@ -47,6 +47,7 @@
 #include "common.hpp"
 #include "grouping.hpp"
 #include "internal.hpp"
+#include "row_copies.hpp"
 
 namespace g355 {
 
@@ -139,40 +140,32 @@ struct KMajorCopy {
 
 // Operand whose rows run along K (BF16): a half is 128 of its columns, each
 // wave copies eight rows of them. The descriptor's base moves with the slice,
-// so that any number of rows can be addressed, and in the last slice its range
-// ends with row K - 1, so that later rows read zeros. A chunk that straddles the last of the
-// tile's `cols` brings in what follows the row, for columns that are never
-// stored. The range check drops a 4-byte word that lies partly past the range,
-// which for an odd column count holds the last element: the range is 2 bytes
-// longer (the host makes sure that those stay on the operand's last page).
+// so that any number of rows can be addressed (row_copies.hpp).
 template <class C, bool PAIRED>
 struct RowsCopy {
   uint32_t off[2][2];
   const char* base;  // of the slice
   int64_t step;      // bytes per slice
-  int ld2, last;     // bytes per row, and of the last row (with the 2 more)
+  uint32_t ld2;      // bytes per row
+  int cols;
   __device__ __forceinline__ void next() { base += step; }
-  __device__ __forceinline__ void point(const char* ptr, int64_t ld, int cols, int, int wave, int lane) {
+  __device__ __forceinline__ void point(const char* ptr, int64_t ld, int cols_, int, int wave, int lane) {
     base = ptr;
+    static_assert(C::ES == 1 || C::BKE <= kSliceRows, "rows_range");
+    ld2 = static_cast<uint32_t>(ld * 2);
     step = ld * 2 * C::BKE;
-    ld2 = static_cast<int>(ld * 2);
-    last = cols * 2 + 2;
+    cols = cols_;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int k = 8 * wave + 4 * q + (lane >> 4);
       const int c = (lane & 15) ^ rows_swizzle<PAIRED>(k);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int n = 128 * h + 8 * c;
-        off[h][q] = n < cols ? static_cast<uint32_t>(k * ld2) + n * 2 : 0x80000000u;
-      }
+      for (int h = 0; h < 2; ++h) off[h][q] = rows_offset(k, ld * 2, 128 * h + 8 * c, cols);
     }
   }
   __device__ __forceinline__ void issue(char* half, int h, int wave, int k0, int K) const {
-    const int rem = K - k0;
-    const int range = rem >= C::BKE ? INT32_MAX : rem > 0 ? (rem - 1) * ld2 + last : 0;
-    const __amdgpu_buffer_rsrc_t rsrc =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, range, kBufferWord3);
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(base), 0, rows_range(K - k0, ld2, cols), kBufferWord3);
 #pragma unroll
     for (int q = 0; q < 2; ++q)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (G355_LDS void*)(half + (2 * wave + q) * 1024),

@@ -12,89 +12,23 @@
 #include <cstdint>
 
 #include "gemm355.h"
+#include "grouped_plan.hpp"
 #include "internal.hpp"
+#include "row_copies.hpp"
 
 using namespace g355;
 
 namespace {
 
-constexpr int kCUs = 256;
 constexpr int64_t kMaxDim = int64_t{1} << 30;
 constexpr int64_t kMaxGroups = int64_t{1} << 16;
 constexpr int64_t k2G = int64_t{1} << 31;
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// Workgroups of a launch over row tiles of bm rows: the most that T rows in
-// min(G, T) non-empty groups can need (each group may waste a partial tile).
-int64_t most_row_tiles(int64_t G, int64_t T, int64_t bm) {
-  return std::min(T, (T + std::min(G, T) * (bm - 1)) / bm);
-}
-
-// Tile of a grouped product. A group of `avg` rows takes avg / bm full tiles
-// and on average half of one more. The costs are microseconds per 128-byte K
-// slice of the slowest CU, from 180 shapes (2 to 32 groups of 32 to 400 rows,
-// N = 1024 and 4096, K = 2048 and 7168, the three types): one tile's slice
-// takes 0.65 us at 64x128 (deep ring), 0.72 at 128x128 (0.95 and 0.9 with B
-// read along its rows), 1.5 at 256x256; two 128x128 tiles on a CU 1.2, two
-// 64x128 tiles 1.05 (1.3). Examples, us at 64x128 / 128x128 / 256x256: BF16, 32
-// groups of 400 rows, 4096 x 7168, 1715 / 1040 / 824; 8 groups of 200, 4096 x
-// 2048, 94 / 40 / 53; 24 groups of a row or two, 2048 x 4096, 64.8 / 78.3; INT8,
-// 30 groups of 4 rows, 4096 x 2048, 47 / 55, of 50 rows 63 / 60.
-GroupedPlan plan_grouped(int64_t G, int64_t T, int64_t N, bool b_rows) {
-  const double groups = static_cast<double>(std::min(G, T));
-  const double avg = static_cast<double>(T) / groups;
-  const auto workgroups = [&](int bm, int bn) {
-    const double row_tiles = avg > 0.5 * bm ? avg / bm + 0.5 : 1.0;
-    return groups * row_tiles * static_cast<double>(ceil_div(N, bn));
-  };
-  // Rounds of the CUs' slots; a last, partial round costs more than its share.
-  const auto rounds = [](double wgs, double slots) {
-    return wgs <= slots ? 1.0 : wgs / slots + 0.2;
-  };
-  const double w128 = workgroups(128, 128);
-  const double w64 = workgroups(64, 128);
-  const double c64 = w64 <= kCUs ? (b_rows ? 0.95 : 0.65) : rounds(w64, 2 * kCUs) * (b_rows ? 1.3 : 1.05);
-  const double c128 = w128 <= kCUs ? (b_rows ? 0.9 : 0.72) : rounds(w128, 2 * kCUs) * 1.2;
-  const double c256 = G <= kTableGroups ? rounds(workgroups(256, 256), kCUs) * 1.5 : 1e30;
-  GroupedPlan best = c64 <= std::min(c128, c256) ? GroupedPlan{64, 128, 0}
-                     : c128 <= c256              ? GroupedPlan{128, 128, 0}
-                                                 : GroupedPlan{256, 256, 0};
-  best.grid = most_row_tiles(G, T, best.bm) * ceil_div(N, best.bn);
-  return best;
-}
-
-// Tile of the weight gradient: G equal grids of N x K outputs, in rounds of the
-// CUs' slots. Measured, us at 256x256 / 128x128: 8 gradients of 14336 x 4096 over
-// 16384 rows 1830 / 2149; 32 of 1000 x 2048 over 777 rows 40 / 53; 1 of 4096 x
-// 4096 over 2000 rows 59 / 75; 4 of 1024 x 1024 over 4000 rows 38 / 22.
-GroupedPlan plan_wgrad(int64_t G, int64_t N, int64_t K) {
-  const auto cost = [&](int b, int occupancy, double eff) {
-    const int64_t wgs = G * ceil_div(N, b) * ceil_div(K, b);
-    return static_cast<double>(ceil_div(wgs, kCUs * occupancy)) * b * b * occupancy / eff;
-  };
-  const int b = cost(256, 1, 0.85) < cost(128, 2, 0.67) ? 256 : 128;
-  const int64_t tiles = ceil_div(N, b) * ceil_div(K, b);
-  return {b, b, G * (tiles >= kWgradXcdTiles ? 8 * ceil_div(tiles, 8) : tiles)};
-}
 
 bool valid_layout(int l) { return l == GEMM_ROW_MAJOR || l == GEMM_COL_MAJOR; }
 bool valid_out(int d) { return d == GEMM_OUT_F32 || d == GEMM_OUT_BF16; }
 bool valid_act(int a) { return a >= GEMM_ACT_NONE && a <= GEMM_ACT_GELU_TANH; }
 bool bad_dim(int64_t v) { return v < 0 || v > kMaxDim; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Whether the DMA loaders of N-major BF16 rows may take an array: rows of ld
-// elements (groups `stride` apart), its last element `last`. They read up to
-// two bytes past that element, in a 4-byte word that holds it: inside the
-// same aligned word where every row starts on one, else on the same page
-// unless the array ends with a page.
-bool rows_dma_ok(const void* p, int64_t ld, int64_t stride, int64_t last) {
-  const uintptr_t base = reinterpret_cast<uintptr_t>(p);
-  if (base & 1u) return false;
-  if (base % 4 == 0 && ld % 2 == 0 && stride % 2 == 0) return true;
-  return (base + 2 * static_cast<uintptr_t>(last + 1)) % 4096 != 0;
-}
 
 int c_vector(const void* C, int64_t ldc, int64_t stride, int c_dtype) {
   return aligned(C, c_dtype == GEMM_OUT_F32 ? 16 : 8) && ldc % 4 == 0 && stride % 4 == 0 ? 1 : 0;
@@ -141,7 +75,7 @@ gemm_status run_grouped(ElemType type, int64_t G, int64_t T, int64_t N, int64_t 
   const bool a_ok = (256 * lda + K) * es < k2G && (bytes1 || aligned(A, 2));
   const bool b_ok = (b_last + 1) * es + 2 < k2G &&
                     (b_kmajor ? bytes1 || aligned(B, 2)
-                              : rows_dma_ok(B, ldb, stride_b, (G - 1) * stride_b + b_last));
+                              : rows_dma_ok(reinterpret_cast<uintptr_t>(B), ldb, stride_b, (G - 1) * stride_b + b_last));
   spec.loader_a = spec.loader_b = LOAD_GENERIC;
   if (K == 0 || (a_ok && b_ok)) {
     spec.loader_a = LOAD_DIRECT;
@@ -250,8 +184,8 @@ gemm_status gemm_grouped_bf16_wgrad(int64_t G, int64_t T, int64_t N, int64_t K, 
   spec.out = c_dtype == GEMM_OUT_F32 ? OUT_F32 : OUT_BF16;
   // DMA: 32-bit offsets into the 64 rows of a slice.
   const bool dma = T == 0 || (128 * std::max(ldd, ldx) < k2G &&
-                              rows_dma_ok(D, ldd, 0, (T - 1) * ldd + N - 1) &&
-                              rows_dma_ok(X, ldx, 0, (T - 1) * ldx + K - 1));
+                              rows_dma_ok(reinterpret_cast<uintptr_t>(D), ldd, 0, (T - 1) * ldd + N - 1) &&
+                              rows_dma_ok(reinterpret_cast<uintptr_t>(X), ldx, 0, (T - 1) * ldx + K - 1));
   spec.loader_a = spec.loader_b = dma ? LOAD_ROWS : LOAD_GENERIC;
   if (!dma) {
     const int64_t tiles = ceil_div(N, 128) * ceil_div(K, 128);

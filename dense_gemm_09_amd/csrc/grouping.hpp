@@ -2,6 +2,7 @@
 #pragma once
 
 #include "common.hpp"
+#include "grouped_plan.hpp"
 
 namespace g355 {
 

@@ -77,10 +77,7 @@ G355_DECLARE_I8(1, 3) G355_DECLARE_I8(1, 4)
 #undef G355_DECLARE_I8
 
 // Products grouped by rows and their weight gradient: FP32 and BF16 output.
-struct GroupedPlan {
-  int bm, bn;    // tile
-  int64_t grid;  // workgroups
-};
+struct GroupedPlan;  // grouped_plan.hpp
 #define G355_GROUPED_LAUNCHER_(r, p) launch_grouped_r##r##_p##p
 #define G355_GROUPED_LAUNCHER(r, p) G355_GROUPED_LAUNCHER_(r, p)
 #define G355_WGRAD_LAUNCHER_(p) launch_wgrad_p##p
