@@ -70,12 +70,14 @@ gemm_status run_grouped(ElemType type, int64_t G, int64_t T, int64_t N, int64_t 
   spec.out = c_dtype == GEMM_OUT_F32 ? OUT_F32 : OUT_BF16;
   spec.a_kmajor = true;
   spec.b_kmajor = b_kmajor;
-  // DMA: 32-bit offsets into a tile's rows of A and into one group's weight.
+  // DMA: 32-bit offsets into a tile's rows of A and into one group's weight, and
+  // 32-bit row distances where the copies follow the rows.
   const int64_t b_last = b_kmajor ? (N - 1) * ldb + K - 1 : (K - 1) * ldb + N - 1;
   const bool a_ok = (256 * lda + K) * es < k2G && (bytes1 || aligned(A, 2));
   const bool b_ok = (b_last + 1) * es + 2 < k2G &&
                     (b_kmajor ? bytes1 || aligned(B, 2)
-                              : rows_dma_ok(reinterpret_cast<uintptr_t>(B), ldb, stride_b, (G - 1) * stride_b + b_last));
+                              : ldb < k2G && rows_dma_ok(reinterpret_cast<uintptr_t>(B), ldb, stride_b,
+                                                         (G - 1) * stride_b + b_last));
   spec.loader_a = spec.loader_b = LOAD_GENERIC;
   if (K == 0 || (a_ok && b_ok)) {
     spec.loader_a = LOAD_DIRECT;

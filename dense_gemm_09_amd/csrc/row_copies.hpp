@@ -15,8 +15,11 @@ namespace g355 {
 constexpr uint32_t kNowhere = 0x80000000u;
 
 // Offset of columns n .. n+7 of row k of the slice; rows are ld2 bytes apart.
+// Rows that the operand has are below 2^31 (see rows_range); where it has fewer
+// than a slice, far apart, the others may not wrap round to one of them.
 constexpr uint32_t rows_offset(int k, int64_t ld2, int n, int cols) {
-  return n < cols ? static_cast<uint32_t>(k * ld2 + n * 2) : kNowhere;
+  const int64_t at = k * ld2 + n * 2;
+  return n < cols && at < kNowhere ? static_cast<uint32_t>(at) : kNowhere;
 }
 
 // Most rows of a slice, and the rows from which on no slice needs a limit: a copy in

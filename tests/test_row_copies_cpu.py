@@ -39,3 +39,10 @@ def test_long_and_far_apart_rows():
     for ld in (1 << 20, (1 << 23) + 3, (1 << 24) - 8):
         for rem in (1, 64, 65, 1000):
             check(rem, ld, 255)
+
+
+def test_few_rows_far_apart():
+    """Rows of the slice past the operand's last, whose offsets pass 32 bits, bring zeros."""
+    for rem, ld in ((2, 1 << 29), (1, (1 << 31) - 1), (5, (1 << 26) + 1), (8, 1 << 26), (33, (1 << 24) + 2)):
+        for cols in (1, 9, 256):
+            check(rem, ld, cols)

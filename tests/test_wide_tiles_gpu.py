@@ -1,6 +1,8 @@
 """Row copies on 256x256 tiles: contraction lengths that fill their last slice, columns that do not fill a chunk."""
 import pytest
+import torch
 
+import dense_gemm_09_amd as g
 from dense_gemm_09_amd import OUT_BF16, OUT_F32, ROW
 from tests import host
 from tests.test_grouped_gpu import gradient, product
@@ -23,3 +25,19 @@ def test_gradient_of_whole_slices(sizes, N, K):
     assert host.lib().wgrad_tile(len(sizes), N, K) == 256
     gradient(sizes, N, K, OUT_F32, ints=3)
     gradient(sizes, N, K, OUT_BF16, seed=2, pad=1)
+
+
+def test_a_weight_of_few_rows_far_apart():
+    """Eight rows of 2^26 elements: what follows them in a slice is zero, not one of them, though one holds an infinity."""
+    T, N, K, ld = 2369, 4096, 8, 1 << 26
+    assert host.lib().grouped_tile(1, T, N, 1) == 256
+    w = torch.zeros((K - 1) * ld + N, dtype=torch.bfloat16, device="cuda")
+    rows = torch.as_strided(w, (K, N), (ld, 1))
+    rows.copy_(torch.randint(-3, 4, (K, N), device="cuda", generator=torch.Generator("cuda").manual_seed(1)))
+    rows[0, 5] = float("inf")
+    x = torch.randint(1, 4, (T, K), device="cuda", generator=torch.Generator("cuda").manual_seed(2)).to(torch.bfloat16)
+    off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    c = torch.empty(T, N, device="cuda")
+    g.gemm_grouped_bf16(1, T, N, K, 1.0, x, K, off, w, ld, ROW, 0, 0.0, c, N, OUT_F32)
+    want = x.cpu().double() @ rows.cpu().double()
+    assert torch.equal(c.cpu().double(), want)
