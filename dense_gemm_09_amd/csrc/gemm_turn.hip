@@ -572,7 +572,10 @@ __global__ void __launch_bounds__(kTurnThreads, 2) gemm_turn_kernel(GemmArgs p) 
     ca.issue(smem + buf * kBuf + h * kHalf, h, wave, ck0, cK);
   };
   const auto copy_b = [&](int buf, int h) __attribute__((always_inline)) {
-    cb.issue(smem + kBBase + buf * kBuf + h * kHalf, h, wave, ck0, cK);
+    // Rows of B that the chunk of A in which K ends belongs to come in the extra
+    // product below: here that chunk is zero, and an infinity or NaN may not meet it.
+    const int end = C::BR && !C::AR ? cK & ~(C::CE - 1) : cK;
+    cb.issue(smem + kBBase + buf * kBuf + h * kHalf, h, wave, ck0, end);
   };
   const auto read_a = [&](auto buf, auto h) __attribute__((always_inline)) {
     ra.template read<decltype(buf)::value * kBuf + decltype(h)::value * kHalf>(fa);

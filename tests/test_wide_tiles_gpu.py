@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import dense_gemm_09_amd as g
-from dense_gemm_09_amd import OUT_BF16, OUT_F32, ROW
+from dense_gemm_09_amd import COL, OUT_BF16, OUT_F32, ROW
 from tests import host
 from tests.test_grouped_gpu import gradient, product
 
@@ -41,3 +41,26 @@ def test_a_weight_of_few_rows_far_apart():
     g.gemm_grouped_bf16(1, T, N, K, 1.0, x, K, off, w, ld, ROW, 0, 0.0, c, N, OUT_F32)
     want = x.cpu().double() @ rows.cpu().double()
     assert torch.equal(c.cpu().double(), want)
+
+
+@pytest.mark.parametrize("K", [4, 8, 61, 63, 64, 66, 77, 130])
+def test_an_infinite_weight_in_any_row(K):
+    """0 * Inf enters no sum: the chunk that K ends inside is multiplied once, by its own values."""
+    N = 4096
+    T = sum(SIZES)
+    off = torch.tensor([0, *torch.tensor(SIZES).cumsum(0).tolist()], dtype=torch.int32)
+    gen = torch.Generator().manual_seed(K)
+    x = torch.randint(1, 4, (T, K), generator=gen).double()
+    w = torch.randint(-3, 4, (len(SIZES), K, N), generator=gen).double()
+    for i in range(len(SIZES)):
+        w[i, K - 1, 3 + i] = float("inf")
+        w[i, max(K - 7, 0), 300 + i] = -float("inf")
+        w[i, 0, 600 + i] = float("inf")
+    want = torch.cat([x[off[i]:off[i + 1]] @ w[i] for i in range(len(SIZES))])
+    assert host.lib().grouped_tile(len(SIZES), T, N, 1) == 256
+    c = torch.empty(T, N, device="cuda")
+    for layout in (ROW, COL):
+        wd = (w if layout == ROW else w.transpose(1, 2)).to(torch.bfloat16).cuda().contiguous()
+        g.gemm_grouped_bf16(len(SIZES), T, N, K, 1.0, x.to(torch.bfloat16).cuda(), K, off.cuda(), wd,
+                            N if layout == ROW else K, layout, N * K, 0.0, c, N, OUT_F32)
+        assert torch.equal(c.cpu().double(), want), layout
