@@ -166,6 +166,10 @@ hipError_t launch_tile(const Plan& plan, const LaunchSpec& spec, const GemmArgs&
                    : spec.out == OUT_BF16 ? PART_BF16
                    : spec.out == OUT_I8   ? PART_I8
                                           : PART_E4M3;
+  // INT8 kernels take 256 rows with 256 columns only. The plans of 8-bit types have
+  // no other tile of 256 rows; one that had would be refused here, before a kernel
+  // counts its columns wrongly.
+  if (spec.i8 && plan.bm == 256 && plan.bn != 256) return hipErrorInvalidValue;
   // The INT8 product's 256x256 tiles, unless their output is partial sums or codes
   // (4096 x 7168 x 2048 with bias and GELU: 84 us, with the tile kernel 93).
   if (spec.i8 && plan.bm == 256 && (part == PART_F32 || part == PART_BF16))
