@@ -1445,8 +1445,12 @@ hipError_t G355_I8_LAUNCHER(G355_RAGGED, G355_PART)(const Plan& plan, const Laun
                           : launch_cfg<NarrowI8, LOAD_DIRECT, LOAD_DIRECT, R>(plan, spec, a, stream);
   if (plan.bm == 128 && plan.grid <= kDeepGrid)
     return launch_cfg<DeepI8, LOAD_DIRECT, LOAD_DIRECT, R>(plan, spec, a, stream);
-  return plan.bm == 256 ? launch_cfg<BigI8, LOAD_DIRECT, LOAD_DIRECT, R>(plan, spec, a, stream)
-                        : launch_cfg<SmallI8, LOAD_DIRECT, LOAD_DIRECT, R>(plan, spec, a, stream);
+  if (plan.bm == 256) {
+    // (256x256 tiles with FP32 or BF16 output are gemm_turn.hip's.)
+    if constexpr (PART == PART_F32 || PART == PART_BF16) return hipErrorInvalidValue;
+    else return launch_cfg<BigI8, LOAD_DIRECT, LOAD_DIRECT, R>(plan, spec, a, stream);
+  }
+  return launch_cfg<SmallI8, LOAD_DIRECT, LOAD_DIRECT, R>(plan, spec, a, stream);
 }
 
 #elif defined(G355_GROUPED)
