@@ -160,6 +160,16 @@ def _need(t, nbytes: int, what: str):
         raise ValueError(f"{what} holds {_nbytes(t)} bytes, the call reads/writes {nbytes}")
 
 
+def _need_int32(t, n: int, what: str):
+    """A vector of n INT32: one of another integer type has the bytes, but is read as other numbers."""
+    if t is None or isinstance(t, int) or n <= 0:
+        return
+    import torch
+    if t.dtype is not torch.int32:
+        raise ValueError(f"{what} must be INT32, not {t.dtype}")
+    _need(t, 4 * n, what)
+
+
 def _extent(rows: int, cols: int, ld: int) -> int:
     """Elements spanned by a rows x cols block stored with leading dimension ld."""
     return 0 if rows == 0 or cols == 0 else (rows - 1) * ld + cols
@@ -299,9 +309,9 @@ def gemm_fp8_scaled_quant(M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, sc
 def _check_int8(M, N, scale_a, zero_a, scale_b, sum_b):
     if M > 0 and N > 0:
         _need(scale_a, 4 * M, "scale_a")
-        _need(zero_a, 4 * M, "zero_a")
+        _need_int32(zero_a, M, "zero_a")
         _need(scale_b, 4 * N, "scale_b")
-        _need(sum_b, 4 * N, "sum_b")
+        _need_int32(sum_b, N, "sum_b")
 
 
 def gemm_int8_scaled(M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, scale_a, zero_a, scale_b,
@@ -329,6 +339,8 @@ def gemm_int8_scaled_quant(M, N, K, alpha, A, lda, layout_a, B, ldb, layout_b, s
     """Q = quant(act(alpha * scale_a[m] scale_b[n] * (A - zero_a[m]) B + bias)) per row, INT8 inputs."""
     L = lib()
     _check_operands(M, N, K, A, lda, layout_a, B, ldb, layout_b, None, ldq, OUT_BF16, 1, bias)
+    if M > 0 and N > 0:
+        _need_int32(out_zero, M, "out_zero")
     _check_quant_out(M, N, Q, ldq, out_scale, out_zero)
     _check_int8(M, N, scale_a, zero_a, scale_b, sum_b)
     workspace, workspace_bytes = _workspace(M, N, K, True, workspace, workspace_bytes, stream)
@@ -345,7 +357,7 @@ def int8_col_sums(K, N, B, ldb, sums, stream=None):
     L = lib()
     if N > 0:
         _need(B, _extent(N, K, ldb), "B")
-        _need(sums, 4 * N, "sums")
+        _need_int32(sums, N, "sums")
     st = L.gemm_int8_col_sums(K, N, _ptr(B), ldb, _ptr(sums), _stream(stream))
     if st != 0:
         raise GemmError(st, "gemm_int8_col_sums")
@@ -357,7 +369,7 @@ def _check_grouped(G, T, N, K, A, lda, offsets, B, ldb, lb, stride_b, C, ldc, c_
             _need(A, esize * _extent(T, K, lda), "A")
             one = _extent(K, N, ldb) if lb == ROW else _extent(N, K, ldb)
             _need(B, esize * ((G - 1) * stride_b + one), "B")
-        _need(offsets, 4 * (G + 1), "offsets")
+        _need_int32(offsets, G + 1, "offsets")
         _need(C, (4 if c_dtype == OUT_F32 else 2) * _extent(T, N, ldc), "C")
         _need(bias, 2 * G * N, "bias")
 
@@ -366,7 +378,7 @@ def gemm_grouped_bf16(G, T, N, K, alpha, A, lda, offsets, B, ldb, layout_b, stri
                       c_dtype, bias=None, act=ACT_NONE, stream=None):
     """C rows offsets[g]..offsets[g+1]-1 = act(alpha * A rows B_g + beta * C rows + bias[g]), BF16.
 
-    offsets: device INT32[G+1]; B_g at B + g * stride_b elements; bias [G, N].
+    offsets: device INT32[G+1] (another type is refused); B_g at B + g * stride_b elements; bias [G, N].
     """
     L = lib()
     _check_grouped(G, T, N, K, A, lda, offsets, B, ldb, layout_b, stride_b, C, ldc, c_dtype, 2, bias)
@@ -413,7 +425,7 @@ def gemm_grouped_bf16_wgrad(G, T, N, K, alpha, D, ldd, X, ldx, offsets, beta, C,
         if T > 0:
             _need(D, 2 * _extent(T, N, ldd), "D")
             _need(X, 2 * _extent(T, K, ldx), "X")
-        _need(offsets, 4 * (G + 1), "offsets")
+        _need_int32(offsets, G + 1, "offsets")
         _need(C, (4 if c_dtype == OUT_F32 else 2) * ((G - 1) * stride_c + _extent(N, K, ldc)), "C")
     st = L.gemm_grouped_bf16_wgrad(G, T, N, K, alpha, _ptr(D), ldd, _ptr(X), ldx, _ptr(offsets),
                                    beta, _ptr(C), ldc, stride_c, c_dtype, _stream(stream))
