@@ -21,11 +21,10 @@ import dense_gemm_09_amd as g  # noqa: E402
 
 def sort_by_expert(x, expert, experts):
     """Rows of x in the order of their expert, that order, and INT32[experts + 1] row offsets."""
-    order = torch.argsort(expert, stable=True)
-    count = torch.bincount(expert, minlength=experts)
-    offsets = torch.zeros(experts + 1, dtype=torch.int32, device=x.device)
-    offsets[1:] = count.cumsum(0)
-    return x[order].contiguous(), order, offsets
+    in_order, order = torch.sort(expert, stable=True)
+    # (Not bincount, which waits for the GPU to size its result.)
+    bounds = torch.arange(experts + 1, device=x.device, dtype=expert.dtype)
+    return x[order].contiguous(), order, torch.searchsorted(in_order, bounds, out_int32=True)
 
 
 def forward(x, w, bias, offsets, act=g.ACT_NONE):
