@@ -171,7 +171,7 @@ hipError_t launch_tile(const Plan& plan, const LaunchSpec& spec, const GemmArgs&
   // counts its columns wrongly.
   if (spec.i8 && plan.bm == 256 && plan.bn != 256) return hipErrorInvalidValue;
   // The INT8 product's 256x256 tiles, unless their output is partial sums or codes
-  // (4096 x 7168 x 2048 with bias and GELU: 84 us, with the tile kernel 93).
+  // (4096 x 7168 x 2048 with bias and GELU: 84 us, where the tile kernel took 93).
   if (spec.i8 && plan.bm == 256 && (part == PART_F32 || part == PART_BF16))
     return launch_turn_i8(spec, plan.grid, args, stream);
   if (spec.i8) return kPartsI8[spec.ragged ? 1 : 0][part](plan, spec, args, stream);

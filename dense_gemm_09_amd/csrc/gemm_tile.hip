@@ -26,7 +26,8 @@
 //   Every iteration issues the same number of DMA instructions (slices past
 //   the end read zeros), so waiting for the oldest slice is a fixed vmcnt.
 // * A BF16 B stored N-contiguous is copied the same way into an N-major tile
-//   (NmajorLoader). Other operands (A column-major, an E4M3 B row-major,
+//   (NmajorLoader), and so are both operands of a weight gradient (RowsLoader).
+//   Other operands (A column-major, an E4M3 B row-major,
 //   operands of 2 GiB or more) are loaded element-wise into registers and
 //   written to the same swizzled layout after the slice's MFMAs.
 // * BF16 uses v_mfma_f32_32x32x16_bf16; FP8 uses v_mfma_scale_f32_32x32x64_f8f6f4
@@ -173,7 +174,10 @@ struct DirectLoader {
 // fetches. Every byte offset is in the per-lane offset (row * ldb * 2 +
 // column * 2, the slice's k0 * ldb * 2 added per slice), so the buffer range
 // check turns rows past the last k and chunks past the array into zeros;
-// chunks at or past N (N is a multiple of 8) get the out-of-range offset.
+// chunks at or past N get the out-of-range offset. The dense product takes N in
+// multiples of 8 and 16-byte aligned rows here; a group's weight has any N and
+// rows at any 2-byte boundary, and a chunk that straddles N brings in what
+// follows the row, for columns that are never stored (row_copies.hpp).
 template <class C, int NW = C::NWAVES>
 struct NmajorLoader {
   static constexpr int ROWN = C::BN * 2;     // bytes per LDS row (one k)
@@ -1455,7 +1459,8 @@ hipError_t G355_I8_LAUNCHER(G355_RAGGED, G355_PART)(const Plan& plan, const Laun
 
 #elif defined(G355_GROUPED)
 
-// One element type's tiles: 128x128 (with a deep ring where a CU has one workgroup), and 64x128.
+// One element type's tiles: 128x128 (with two K groups where a CU has one workgroup), and 64x128
+// (with a ring of six slices there, of three where it has two).
 template <class SMALL, class DEEP, class NARROW, class PAIR, int LB>
 static hipError_t launch_grouped_type(const GroupedPlan& plan, const GemmArgs& a,
                                       hipStream_t stream) {

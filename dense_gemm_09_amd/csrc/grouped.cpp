@@ -4,7 +4,7 @@
 // The groups' row ranges are device data (they come out of a router on the
 // GPU), so everything here is decided from what the host knows: the number of
 // groups, the rows in all, and the sizes of a weight. The kernels find each
-// workgroup's group themselves (gemm_tile.hip, find_group).
+// workgroup's group themselves (grouping.hpp).
 
 #include <hip/hip_runtime.h>
 

@@ -34,7 +34,7 @@ inline int64_t most_row_tiles(int64_t G, int64_t T, int64_t bm) {
 // and on average half of one more. The costs are microseconds per 128-byte K
 // slice of the slowest CU, from 180 shapes (2 to 32 groups of 32 to 400 rows,
 // N = 1024 and 4096, K = 2048 and 7168, the three types): one tile's slice
-// takes 0.65 us at 64x128 (deep ring), 0.72 at 128x128 (0.95 and 0.9 with B
+// takes 0.65 us at 64x128 (ring of six slices), 0.72 at 128x128 (0.95 and 0.9 with B
 // read along its rows), 1.5 at 256x256; two 128x128 tiles on a CU 1.2, two
 // 64x128 tiles 1.05 (1.3). Examples, us at 64x128 / 128x128 / 256x256: BF16, 32
 // groups of 400 rows, 4096 x 7168, 1715 / 1040 / 824; 8 groups of 200, 4096 x

@@ -19,8 +19,8 @@ enum TileMode : int { MODE_DENSE = 0, MODE_GROUPED = 1, MODE_WGRAD = 2 };
 
 // Tile rows that a group's tiles are numbered along before the next column: the
 // tiles in flight on an XCD share that many row panels, and a group of that many
-// tile rows has its weight read once (16384 x 14336 x 4096 over 8 experts: 1736 us
-// with 2, 1645 with 4, 1617 with 8).
+// tile rows has its weight read once (16384 x 14336 x 4096 over 8 experts, in one
+// run: 1736 us with 2, 1645 with 4, 1617 with 8).
 constexpr int kGroupedBand = 8;
 
 // Group g's rows [s, e). The offsets are device data that no host check has

@@ -13,9 +13,10 @@ namespace g355 {
 enum Loader : int {
   LOAD_DIRECT = 0,   // K-major, 16-byte aligned rows: global -> LDS DMA, no registers
   LOAD_GENERIC = 1,  // any layout / alignment: element loads through registers
-  LOAD_DIRECT_N = 2, // B only, BF16 N-contiguous (row-major), 16-byte aligned rows, N % 8 == 0:
-                     // DMA into an N-major LDS tile, fragments by transposing LDS reads
-  LOAD_ROWS = 3,     // both operands of the weight gradient: as LOAD_DIRECT_N, any 2-byte alignment
+  LOAD_DIRECT_N = 2, // B only, BF16 N-contiguous (row-major): DMA into an N-major LDS tile, fragments by
+                     // transposing LDS reads. Dense products: 16-byte aligned rows, N % 8 == 0; grouped
+                     // ones: any N and any 2-byte alignment
+  LOAD_ROWS = 3,     // both operands of the weight gradient: the same, an operand of any size
 };
 
 enum KernelKind : int { KERNEL_TILE = 0, KERNEL_SKINNY = 1 };
