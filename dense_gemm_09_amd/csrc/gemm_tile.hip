@@ -1465,9 +1465,14 @@ template <class SMALL, class DEEP, class NARROW, class PAIR, int LB>
 static hipError_t launch_grouped_type(const GroupedPlan& plan, const GemmArgs& a,
                                       hipStream_t stream) {
   constexpr bool R = G355_RAGGED != 0;
-  if (plan.bm == 64)
-    return plan.grid <= kDeepGrid ? launch_grouped<NARROW, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream)
-                                  : launch_grouped<PAIR, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
+  if (plan.bm == 64) {
+    // (plan_grouped: not with B read along its rows.)
+    if constexpr (LB == LOAD_DIRECT_N)
+      return hipErrorInvalidValue;
+    else
+      return plan.grid <= kDeepGrid ? launch_grouped<NARROW, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream)
+                                    : launch_grouped<PAIR, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
+  }
   if (plan.grid <= kDeepGrid) return launch_grouped<DEEP, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
   return launch_grouped<SMALL, LOAD_DIRECT, LB, R, MODE_GROUPED>(plan.grid, a, stream);
 }

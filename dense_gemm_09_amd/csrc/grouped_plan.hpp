@@ -34,9 +34,10 @@ inline int64_t most_row_tiles(int64_t G, int64_t T, int64_t bm) {
 // and on average half of one more. The costs are microseconds per 128-byte K
 // slice of the slowest CU, from 180 shapes (2 to 32 groups of 32 to 400 rows,
 // N = 1024 and 4096, K = 2048 and 7168, the three types): one tile's slice
-// takes 0.65 us at 64x128 (ring of six slices), 0.72 at 128x128 (0.95 and 0.9 with B
-// read along its rows), 1.5 at 256x256; two 128x128 tiles on a CU 1.2, two
-// 64x128 tiles 1.05 (1.3). Examples, us at 64x128 / 128x128 / 256x256: BF16, 32
+// takes 0.65 us at 64x128 (ring of six slices), 0.72 at 128x128, 1.5 at 256x256; two
+// 128x128 tiles on a CU 1.2, two 64x128 tiles 1.05. With B read along its rows, 0.9
+// at 128x128 and 0.95 at 64x128 (two: 1.3): no kernel of 64 rows there, as 128 rows
+// are never more workgroups. Examples, us at 64x128 / 128x128 / 256x256: BF16, 32
 // groups of 400 rows, 4096 x 7168, 1715 / 1040 / 824; 8 groups of 200, 4096 x
 // 2048, 94 / 40 / 53; 24 groups of a row or two, 2048 x 4096, 64.8 / 78.3; INT8,
 // 30 groups of 4 rows, 4096 x 2048, 47 / 55, of 50 rows 63 / 60.
@@ -53,7 +54,9 @@ inline GroupedPlan plan_grouped(int64_t G, int64_t T, int64_t N, bool b_rows) {
   };
   const double w128 = workgroups(128, 128);
   const double w64 = workgroups(64, 128);
-  const double c64 = w64 <= kGroupedCUs ? (b_rows ? 0.95 : 0.65) : rounds(w64, 2 * kGroupedCUs) * (b_rows ? 1.3 : 1.05);
+  const double c64 = b_rows              ? 1e30
+                     : w64 <= kGroupedCUs ? 0.65
+                                          : rounds(w64, 2 * kGroupedCUs) * 1.05;
   const double c128 = w128 <= kGroupedCUs ? (b_rows ? 0.9 : 0.72) : rounds(w128, 2 * kGroupedCUs) * 1.2;
   const double c256 = G <= kTableGroups ? rounds(workgroups(256, 256), kGroupedCUs) * 1.5 : 1e30;
   GroupedPlan best = c64 <= std::min(c128, c256) ? GroupedPlan{64, 128, 0}
