@@ -64,3 +64,22 @@ def test_an_infinite_weight_in_any_row(K):
         g.gemm_grouped_bf16(len(SIZES), T, N, K, 1.0, x.to(torch.bfloat16).cuda(), K, off.cuda(), wd,
                             N if layout == ROW else K, layout, N * K, 0.0, c, N, OUT_F32)
         assert torch.equal(c.cpu().double(), want), layout
+
+
+@pytest.mark.parametrize("sizes,N", [([0, 1, 5, 0, 64, 65, 2], 200), ([130, 0, 257, 300, 1], 2048), ([130, 0, 257], 8192)])
+@pytest.mark.parametrize("K", [61, 77])
+def test_an_infinite_weight_on_smaller_tiles(sizes, N, K):
+    """The same weight gives the same infinities whatever tile the call is planned on."""
+    G, T = len(sizes), sum(sizes)
+    assert host.lib().grouped_tile(G, T, N, 1) == 128
+    gen = torch.Generator().manual_seed(K)
+    x = torch.randint(1, 4, (T, K), generator=gen).double()
+    w = torch.randint(-3, 4, (G, K, N), generator=gen).double()
+    w[:, K - 1, 3] = float("inf")
+    w[:, K - 5, 100] = -float("inf")
+    off = [0, *torch.tensor(sizes).cumsum(0).tolist()]
+    want = torch.cat([x[off[i]:off[i + 1]] @ w[i] for i in range(G)])
+    c = torch.empty(T, N, device="cuda")
+    g.gemm_grouped_bf16(G, T, N, K, 1.0, x.to(torch.bfloat16).cuda(), K, torch.tensor(off, dtype=torch.int32).cuda(),
+                        w.to(torch.bfloat16).cuda(), N, ROW, N * K, 0.0, c, N, OUT_F32)
+    assert torch.equal(c.cpu().double(), want)
