@@ -245,8 +245,8 @@ struct RowsLoader {
   int64_t ld2;  // bytes per row
   int cols;
 
-  __device__ __forceinline__ void init(const void* ptr, int64_t ld, int col0, int cols_, int wave,
-                                       int lane) {
+  __device__ __forceinline__ void init(const void* ptr, int64_t ld, int col0, int cols_, int K,
+                                       int wave, int lane) {
     base = static_cast<const char*>(ptr);
     ld2 = ld * 2;
     cols = cols_;
@@ -254,7 +254,7 @@ struct RowsLoader {
     for (int i = 0; i < IPW; ++i) {
       const int r = (wave * IPW + i) * RPSN + lane / CPRN;
       const int lc = (lane % CPRN) ^ (4 * (r & 3));
-      off[i] = rows_offset(r, ld2, col0 + 8 * lc, cols);
+      off[i] = rows_offset(r, static_cast<uint32_t>(ld2), col0 + 8 * lc, cols, K);
     }
   }
 
@@ -751,7 +751,7 @@ gemm_tile_kernel(GemmArgs p) {
   if constexpr (LA == LOAD_DIRECT) {
     da.init(p.lda, m0, p.M, wave, lane);
   } else if constexpr (LA == LOAD_ROWS) {
-    ra.init(p.A, p.lda, m0, p.M, wave, lane);
+    ra.init(p.A, p.lda, m0, p.M, p.K, wave, lane);
   } else {
     ga.base = static_cast<const char*>(p.A); ga.ld = p.lda; ga.row0 = m0; ga.rows = p.M;
     ga.kmajor = p.a_mn_major == 0;
@@ -776,7 +776,7 @@ gemm_tile_kernel(GemmArgs p) {
   } else if constexpr (LB == LOAD_DIRECT_N) {
     dn.init(p.ldb, n0, p.N, ext_b, wave, lane);
   } else if constexpr (LB == LOAD_ROWS) {
-    rb.init(p.B, p.ldb, n0, p.N, wave, lane);
+    rb.init(p.B, p.ldb, n0, p.N, p.K, wave, lane);
   } else {
     gb.base = static_cast<const char*>(p.B); gb.ld = p.ldb; gb.row0 = n0; gb.rows = p.N;
     gb.kmajor = p.b_mn_major == 0;

@@ -149,7 +149,7 @@ struct RowsCopy {
   uint32_t ld2;      // bytes per row
   int cols;
   __device__ __forceinline__ void next() { base += step; }
-  __device__ __forceinline__ void point(const char* ptr, int64_t ld, int cols_, int, int wave, int lane) {
+  __device__ __forceinline__ void point(const char* ptr, int64_t ld, int cols_, int K, int wave, int lane) {
     base = ptr;
     static_assert(C::ES == 1 || C::BKE <= kSliceRows, "rows_range");
     ld2 = static_cast<uint32_t>(ld * 2);
@@ -160,7 +160,7 @@ struct RowsCopy {
       const int k = 8 * wave + 4 * q + (lane >> 4);
       const int c = (lane & 15) ^ rows_swizzle<PAIRED>(k);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) off[h][q] = rows_offset(k, ld * 2, 128 * h + 8 * c, cols);
+      for (int h = 0; h < 2; ++h) off[h][q] = rows_offset(k, ld2, 128 * h + 8 * c, cols, K);
     }
   }
   __device__ __forceinline__ void issue(char* half, int h, int wave, int k0, int K) const {

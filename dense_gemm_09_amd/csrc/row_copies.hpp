@@ -14,12 +14,12 @@ namespace g355 {
 // Offset of a copy that brings zeros: past every range.
 constexpr uint32_t kNowhere = 0x80000000u;
 
-// Offset of columns n .. n+7 of row k of the slice; rows are ld2 bytes apart.
-// Rows that the operand has are below 2^31 (see rows_range); where it has fewer
-// than a slice, far apart, the others may not wrap round to one of them.
-constexpr uint32_t rows_offset(int k, int64_t ld2, int n, int cols) {
-  const int64_t at = k * ld2 + n * 2;
-  return n < cols && at < kNowhere ? static_cast<uint32_t>(at) : kNowhere;
+// Offset of columns n .. n+7 of row k of a slice; rows are ld2 bytes apart, K in
+// all. 64 rows, or all that there are, span less than 2^31 bytes (the host checks
+// it), and where K is shorter than a slice the rows past it get no offset: far
+// apart, theirs would wrap round to a row that exists.
+constexpr uint32_t rows_offset(int k, uint32_t ld2, int n, int cols, int K) {
+  return n < cols && k < K ? static_cast<uint32_t>(k) * ld2 + static_cast<uint32_t>(n * 2) : kNowhere;
 }
 
 // Most rows of a slice, and the rows from which on no slice needs a limit: a copy in
@@ -28,8 +28,7 @@ constexpr int kSliceRows = 64;
 constexpr int kFreeRows = kSliceRows + 8;
 
 // Range of the descriptor of a slice with `rem` rows up to the end of K, `cols`
-// columns from its base; 64 rows, or all that there are, span less than 2^31
-// bytes (the host checks it). Where the operand ends, the range ends with row
+// columns from its base. Where the operand ends, the range ends with row
 // rem - 1: later rows then read zeros, and a chunk that straddles the last column
 // of the last row reads no word past that column (in the rows before, it reads
 // what follows the row, into columns that are never stored). For an odd number

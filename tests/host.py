@@ -19,7 +19,7 @@ def lib():
         assert r.returncode == 0, r.stderr
         L = ctypes.CDLL(so)
     i, q = ctypes.c_int, ctypes.c_int64
-    L.check_slice.argtypes = [i, i, q, i, q]
+    L.check_slice.argtypes = [i, i, i, q, i, q]
     L.grouped_tile.argtypes = [q, q, q, i]
     L.wgrad_tile.argtypes = [q, q, q]
     return L

@@ -20,12 +20,12 @@ enum : int { OVER_READ = 1, LOST = 2, NOT_ZERO = 4, NEXT_PAGE = 8 };
 
 extern "C" {
 
-// The copies of one slice of an operand of `cols` columns whose first row is at
-// byte `base` (mod 4096): `rows` rows of the slice's place in LDS, `rem` rows of the
-// operand. Returns a set of: a word more than 2 bytes past the last element is
+// The copies of one slice of an operand of `cols` columns and K rows, whose first
+// row is at byte `base` (mod 4096): `rows` rows of the slice's place in LDS, `rem` rows
+// of the operand from the slice on. Returns a set of: a word more than 2 bytes past the last element is
 // read; an element is not; an element of a row past `rem` is; a byte on the
 // page after the last element's is read although rows_dma_ok admits the array.
-int check_slice(int rows, int rem, int64_t ld, int cols, int64_t base) {
+int check_slice(int rows, int rem, int K, int64_t ld, int cols, int64_t base) {
   int bad = 0;
   const int64_t ld2 = 2 * ld;
   const int range = rows_range(rem, static_cast<uint32_t>(ld2), cols);
@@ -33,7 +33,7 @@ int check_slice(int rows, int rem, int64_t ld, int cols, int64_t base) {
   const bool ok = rows_dma_ok(static_cast<uintptr_t>(base), ld, 0, rem > 0 ? end / 2 - 1 : 0);
   for (int k = 0; k < rows; ++k) {
     for (int n = 0; n < (cols + 15) / 8 * 8; n += 8) {
-      const uint32_t off = rows_offset(k, ld2, n, cols);
+      const uint32_t off = rows_offset(k, static_cast<uint32_t>(ld2), n, cols, K);
       for (int w = 0; w < 4; ++w) {
         const bool in = admitted(off, w, range);
         const int64_t to = static_cast<int64_t>(off) + 4 * w + 4;

@@ -12,10 +12,12 @@ OVER_READ, LOST, NOT_ZERO, NEXT_PAGE = 1, 2, 4, 8
 
 
 def check(rem, ld, cols, base=0):
-    bad = host.lib().check_slice(64, rem, ld, cols, base)
-    names = [n for n, b in (("reads past the operand", 1), ("loses an element", 2),
-                            ("reads rows past the last", 4), ("reads the next page", 8)) if bad & b]
-    assert not bad, f"rem={rem} ld={ld} cols={cols} base={base}: {', '.join(names)}"
+    # As the first slice, and as a later one of an operand whose first 64 rows lie within 2^31 bytes.
+    for K in (rem, rem + 64) if 128 * ld < 1 << 31 else (rem,):
+        bad = host.lib().check_slice(64, rem, K, ld, cols, base)
+        names = [n for n, b in (("reads past the operand", 1), ("loses an element", 2),
+                                ("reads rows past the last", 4), ("reads the next page", 8)) if bad & b]
+        assert not bad, f"rem={rem} K={K} ld={ld} cols={cols} base={base}: {', '.join(names)}"
 
 
 @pytest.mark.parametrize("rem", [0, 1, 2, 31, 63, 64, 65, 66, 71, 72, 73, 127, 128, 129, 1000])
