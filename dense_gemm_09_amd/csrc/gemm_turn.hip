@@ -32,11 +32,12 @@
 //   are in flight while this one's epilogue runs (8 experts' forward pass, no
 //   activation, 1602 -> 1543 us; short products lose nothing).
 //
-// Measured, all three at 16384 rows over 8 experts, 14336 x 4096: forward with bias
-// and GELU 1560 us (1230 TFLOP/s), the same without them 1380 us, weight gradient
-// in FP32 1700 us. The matrix cores are busy 64% of the cycles and the card runs
-// at its power limit, at 1.65 GHz; GELU is vector arithmetic that nothing
-// overlaps (120 us), stores and their acknowledgement cost 6 us a tile.
+// Measured at 16384 rows over 8 experts, 14336 x 4096, calls over changing inputs,
+// one run: forward with bias and GELU 1662 us (1158 TFLOP/s; without them 1572),
+// weight gradient in FP32 1780 us. The matrix cores are busy 65% and 55% of the
+// cycles and the card runs at its power limit, at 1.6 to 1.8 GHz; GELU is vector
+// arithmetic that nothing overlaps (120 us), stores and their acknowledgement cost
+// 6 us a tile.
 //
 // Operands that are contiguous along the other axis (the weight of an input
 // gradient, both operands of a weight gradient) are copied as they lie: LDS
