@@ -22,6 +22,7 @@ ROW, COL = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
 QOUT_INT8, QOUT_E4M3 = 0, 1
 ACT_NONE, ACT_RELU, ACT_GELU_ERF, ACT_GELU_TANH = 0, 1, 2, 3
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 STATUS = ["GEMM_OK", "GEMM_ERR_NULL_POINTER", "GEMM_ERR_BAD_DIM", "GEMM_ERR_BAD_LD",
           "GEMM_ERR_BAD_ENUM", "GEMM_ERR_UNSUPPORTED", "GEMM_ERR_WORKSPACE_TOO_SMALL",
@@ -30,7 +31,9 @@ EXPORTS = ["gemm_bf16", "gemm_bf16_noalloc", "gemm_fp8_scaled", "gemm_mxfp8", "g
            "gemm_int8_scaled", "gemm_int8_scaled_quant", "gemm_quantize_int8_rows",
            "gemm_int8_col_sums", "gemm_grouped_bf16", "gemm_grouped_fp8_scaled",
            "gemm_grouped_int8_scaled", "gemm_grouped_bf16_wgrad",
-           "gemm_quantize_fp8_rows", "gemm_pack_b", "gemm_workspace_size", "gemm_plan",
+           "gemm_route", "gemm_route_grad", "gemm_route_order", "gemm_route_order_workspace_size",
+           "gemm_dispatch_rows", "gemm_combine_rows", "gemm_combine_rows_grad", "gemm_lora_bf16",
+           "gemm_lora_workspace_size", "gemm_quantize_fp8_rows", "gemm_pack_b", "gemm_workspace_size", "gemm_plan",
            "gemm_status_string"]
 
 
@@ -104,6 +107,30 @@ def lib() -> ctypes.CDLL:
         L.gemm_grouped_bf16_wgrad.restype = _I32
         L.gemm_grouped_bf16_wgrad.argtypes = [_I64, _I64, _I64, _I64, _F32, _P, _I64, _P, _I64, _P,
                                               _F32, _P, _I64, _I64, _I32, _P]
+        L.gemm_route.restype = _I32
+        L.gemm_route.argtypes = [_I64, _I64, _I64, _P, _I64, _I32, _I32, _P, _I64, _I64, _I32, _I32,
+                                 _F32, _P, _P, _P]
+        L.gemm_route_grad.restype = _I32
+        L.gemm_route_grad.argtypes = [_I64, _I64, _I64, _P, _I64, _I32, _I32, _I32, _F32, _P, _P, _P,
+                                      _I64, _P]
+        L.gemm_route_order.restype = _I32
+        L.gemm_route_order.argtypes = [_I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]
+        L.gemm_route_order_workspace_size.restype = _SZ
+        L.gemm_route_order_workspace_size.argtypes = [_I64, _I64]
+        L.gemm_dispatch_rows.restype = _I32
+        L.gemm_dispatch_rows.argtypes = [_I64, _I64, _I64, _I64, _P, _I64, _I32, _P, _P, _I64, _P]
+        L.gemm_combine_rows.restype = _I32
+        L.gemm_combine_rows.argtypes = [_I64, _I64, _I64, _I64, _P, _I64, _I32, _P, _P, _F32, _P,
+                                        _I64, _I32, _P]
+        L.gemm_combine_rows_grad.restype = _I32
+        L.gemm_combine_rows_grad.argtypes = [_I64, _I64, _I64, _I64, _P, _I64, _I32, _P, _I64, _I32,
+                                             _P, _P, _P, _I64, _P, _P]
+        L.gemm_lora_bf16.restype = _I32
+        L.gemm_lora_bf16.argtypes = [_I64, _I64, _I64, _I64, _I64, _F32, _P, _I64, _P, _I64, _P, _P,
+                                     _I64, _I64, _P, _I64, _I64, _P, _F32, _P, _I64, _I32, _P, _I32,
+                                     _P, _SZ, _P]
+        L.gemm_lora_workspace_size.restype = _SZ
+        L.gemm_lora_workspace_size.argtypes = [_I64, _I64, _I64, _I64]
         L.gemm_pack_b.restype = _I32
         L.gemm_pack_b.argtypes = [_I64, _I64, _P, _I64, _I32, _I32, _P, _I64, _P]
         L.gemm_quantize_fp8_rows.restype = _I32
@@ -167,6 +194,16 @@ def _need_int32(t, n: int, what: str):
     import torch
     if t.dtype is not torch.int32:
         raise ValueError(f"{what} must be INT32, not {t.dtype}")
+    _need(t, 4 * n, what)
+
+
+def _need_f32(t, n: int, what: str):
+    """A vector of n FP32."""
+    if t is None or isinstance(t, int) or n <= 0:
+        return
+    import torch
+    if t.dtype is not torch.float32:
+        raise ValueError(f"{what} must be FP32, not {t.dtype}")
     _need(t, 4 * n, what)
 
 
@@ -433,6 +470,137 @@ def gemm_grouped_bf16_wgrad(G, T, N, K, alpha, D, ldd, X, ldx, offsets, beta, C,
         raise GemmError(st, "gemm_grouped_bf16_wgrad")
 
 
+def _size(dtype: int) -> int:
+    return 4 if dtype == OUT_F32 else 2
+
+
+def route(T, E, top_k, logits, ldl, l_dtype, score, bias, groups, top_groups, group_best, renormalise, scale,
+          expert, weight, stream=None):
+    """The top_k experts of every token (INT32[T, top_k], -1 where none is left) and their FP32 weights.
+
+    logits: T rows of E, FP32 or BF16; score: SCORE_SOFTMAX or SCORE_SIGMOID; bias: FP32[E] or None, added to
+    the scores for the choice alone; experts outside the top_groups best of `groups` groups are not chosen.
+    """
+    L = lib()
+    if T > 0 and E > 0 and top_k > 0:
+        _need(logits, _size(l_dtype) * _extent(T, E, ldl), "logits")
+        _need_f32(bias, E, "bias")
+        _need_int32(expert, T * top_k, "expert")
+        _need_f32(weight, T * top_k, "weight")
+    st = L.gemm_route(T, E, top_k, _ptr(logits), ldl, l_dtype, score, _ptr(bias), groups, top_groups, group_best,
+                      1 if renormalise else 0, scale, _ptr(expert), _ptr(weight), _stream(stream))
+    if st != 0:
+        raise GemmError(st, "gemm_route")
+
+
+def route_grad(T, E, top_k, logits, ldl, l_dtype, score, renormalise, scale, expert, dweight, dlogits, ldd,
+               stream=None):
+    """dlogits (the logits' type, all E columns): the gradient of route's weights, the choice held fixed."""
+    L = lib()
+    if T > 0 and E > 0 and top_k > 0:
+        _need(logits, _size(l_dtype) * _extent(T, E, ldl), "logits")
+        _need_int32(expert, T * top_k, "expert")
+        _need_f32(dweight, T * top_k, "dweight")
+        _need(dlogits, _size(l_dtype) * _extent(T, E, ldd), "dlogits")
+    st = L.gemm_route_grad(T, E, top_k, _ptr(logits), ldl, l_dtype, score, 1 if renormalise else 0, scale,
+                           _ptr(expert), _ptr(dweight), _ptr(dlogits), ldd, _stream(stream))
+    if st != 0:
+        raise GemmError(st, "gemm_route_grad")
+
+
+def route_order_workspace_size(S: int, G: int) -> int:
+    return int(lib().gemm_route_order_workspace_size(S, G))
+
+
+def route_order(S, G, expert, offsets, position, order=None, workspace=None, workspace_bytes=None, stream=None):
+    """Slots sorted stably by expert: offsets INT32[G + 1], the row of each slot (-1: no expert), and the slot of
+    each row (-1 behind the last). With workspace=None one is allocated on the call's stream."""
+    L = lib()
+    if S >= 0 and G >= 0:
+        _need_int32(expert, S, "expert")
+        _need_int32(offsets, G + 1, "offsets")
+        _need_int32(position, S, "position")
+        _need_int32(order, S, "order")
+    workspace, workspace_bytes = _scratch(route_order_workspace_size(S, G), workspace, workspace_bytes, stream)
+    st = L.gemm_route_order(S, G, _ptr(expert), _ptr(offsets), _ptr(position), _ptr(order), _ptr(workspace),
+                            workspace_bytes, _stream(stream))
+    if st != 0:
+        raise GemmError(st, "gemm_route_order")
+
+
+def dispatch_rows(T, top_k, R, N, X, ldx, elem_bytes, position, Y, ldy, stream=None):
+    """Y[position[t, j]] = X[t]: rows of N elements of 1, 2 or 4 bytes; positions outside [0, R) are passed over."""
+    L = lib()
+    if T > 0 and top_k > 0 and R > 0 and N > 0:
+        _need(X, elem_bytes * _extent(T, N, ldx), "X")
+        _need_int32(position, T * top_k, "position")
+        _need(Y, elem_bytes * _extent(R, N, ldy), "Y")
+    st = L.gemm_dispatch_rows(T, top_k, R, N, _ptr(X), ldx, elem_bytes, _ptr(position), _ptr(Y), ldy,
+                              _stream(stream))
+    if st != 0:
+        raise GemmError(st, "gemm_dispatch_rows")
+
+
+def combine_rows(T, top_k, R, N, Y, ldy, y_dtype, position, weight, beta, C, ldc, c_dtype, stream=None):
+    """C[t] = sum_j weight[t, j] * Y[position[t, j]] + beta * C[t] (weight None: ones), summed in FP32."""
+    L = lib()
+    if T > 0 and top_k > 0 and N > 0:
+        _need(Y, _size(y_dtype) * _extent(R, N, ldy), "Y")
+        _need_int32(position, T * top_k, "position")
+        _need_f32(weight, T * top_k, "weight")
+        _need(C, _size(c_dtype) * _extent(T, N, ldc), "C")
+    st = L.gemm_combine_rows(T, top_k, R, N, _ptr(Y), ldy, y_dtype, _ptr(position), _ptr(weight), beta, _ptr(C), ldc,
+                             c_dtype, _stream(stream))
+    if st != 0:
+        raise GemmError(st, "gemm_combine_rows")
+
+
+def combine_rows_grad(T, top_k, R, N, D, ldd, d_dtype, Y, ldy, y_dtype, position, weight, dY, lddy, dweight=None,
+                      stream=None):
+    """dY[position[t, j]] = weight[t, j] * D[t] and dweight[t, j] = <D[t], Y[position[t, j]]> (None: not formed)."""
+    L = lib()
+    if T > 0 and top_k > 0:
+        if N > 0 and R > 0:
+            _need(D, _size(d_dtype) * _extent(T, N, ldd), "D")
+            if dweight is not None:
+                _need(Y, _size(y_dtype) * _extent(R, N, ldy), "Y")
+            _need(dY, _size(y_dtype) * _extent(R, N, lddy), "dY")
+        _need_int32(position, T * top_k, "position")
+        _need_f32(weight, T * top_k, "weight")
+        _need_f32(dweight, T * top_k, "dweight")
+    st = L.gemm_combine_rows_grad(T, top_k, R, N, _ptr(D), ldd, d_dtype, _ptr(Y), ldy, y_dtype, _ptr(position),
+                                  _ptr(weight), _ptr(dY), lddy, _ptr(dweight), _stream(stream))
+    if st != 0:
+        raise GemmError(st, "gemm_combine_rows_grad")
+
+
+def lora_workspace_size(M: int, N: int, K: int, R: int) -> int:
+    return int(lib().gemm_lora_workspace_size(M, N, K, R))
+
+
+def gemm_lora_bf16(M, N, K, G, R, alpha, A, lda, B, ldb, adapter, down, ld_down, stride_down, up, ld_up, stride_up,
+                   scale, beta, C, ldc, c_dtype, bias=None, act=ACT_NONE, workspace=None, workspace_bytes=None,
+                   stream=None):
+    """C = act(alpha * (A B + scale[a] * (A down_a) up_a) + beta * C + bias), a = adapter[m] of each row.
+
+    A: M rows of K, B: N rows of K (COL), BF16; adapter: INT32[M], rows outside [0, G) have none; down: G times R
+    rows of K, up: G times N rows of R; scale: FP32[G] or None. With workspace=None one is allocated here.
+    """
+    L = lib()
+    _check_operands(M, N, K, A, lda, ROW, B, ldb, COL, C, ldc, c_dtype, 2, bias)
+    if M > 0 and N > 0 and G > 0 and R > 0:
+        _need_int32(adapter, M, "adapter")
+        _need(down, 2 * ((G - 1) * stride_down + _extent(R, K, ld_down)) if K > 0 else 0, "down")
+        _need(up, 2 * ((G - 1) * stride_up + _extent(N, R, ld_up)), "up")
+        _need_f32(scale, G, "scale")
+    workspace, workspace_bytes = _scratch(lora_workspace_size(M, N, K, R), workspace, workspace_bytes, stream)
+    st = L.gemm_lora_bf16(M, N, K, G, R, alpha, _ptr(A), lda, _ptr(B), ldb, _ptr(adapter), _ptr(down), ld_down,
+                          stride_down, _ptr(up), ld_up, stride_up, _ptr(scale), beta, _ptr(C), ldc, c_dtype,
+                          _ptr(bias), act, _ptr(workspace), workspace_bytes, _stream(stream))
+    if st != 0:
+        raise GemmError(st, "gemm_lora_bf16")
+
+
 def pack_b(K, N, B, ldb, layout_b, elem_bytes, Bp, ldbp, stream=None):
     """One-time reorder of B (K x N) into K-major rows: Bp[n*ldbp + k] = b(k, n)."""
     L = lib()
@@ -481,8 +649,15 @@ def _torch_stream(stream):
 
 
 def _workspace(M, N, K, fp8, workspace, workspace_bytes, stream):
+    need = 0
     if workspace is None:
         need = workspace_size(M, N, K, fp8) if M >= 0 and N >= 0 and K >= 0 else 0
+    return _scratch(need, workspace, workspace_bytes, stream)
+
+
+def _scratch(need, workspace, workspace_bytes, stream):
+    """The caller's workspace and its size, or one of `need` bytes."""
+    if workspace is None:
         if need == 0:
             return None, 0
         import torch

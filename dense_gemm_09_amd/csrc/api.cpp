@@ -52,7 +52,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int64_t kThinMaxM = 64;
 
 // Tile-kernel plan (any M): tile shape and split from the cost model.
-static Plan make_tile_plan(int64_t M, int64_t N, int64_t K, bool fp8) {
+Plan make_tile_plan(int64_t M, int64_t N, int64_t K, bool fp8) {
   const int bke = fp8 ? 128 : 64;
   const double flops_per_clk = fp8 ? 8192.0 : 4096.0;  // per CU, dense
   const double clk = 2.4e9;

@@ -41,6 +41,7 @@
 #include "common.hpp"
 #include "grouping.hpp"
 #include "internal.hpp"
+#include "lora.hpp"
 #include "row_copies.hpp"
 
 namespace g355 {
@@ -663,14 +664,75 @@ __device__ __forceinline__ void run_epilogue(const GemmArgs& p,
   }
 }
 
+// ------------------------------------------------------------ low-rank adapters
+
+// acc += h up_a for a wave's rows, a being the row's adapter: what the first
+// factors' product left in p.h times the second factors, on the same MFMA and
+// accumulator layout as the main product. Block row by block row (32 rows), once for
+// every adapter in it: neighbours mostly share one. Every adapter's product has
+// an accumulator of its own, from which the rows that have that adapter are
+// taken, so that an adapter's infinities and NaN reach no other row.
+// Fragments come straight from memory: h is small and stays in cache, and a
+// tile's columns of an adapter are read by the waves of one tile row.
+template <class C>
+__device__ __forceinline__ void add_adapters(const LoraArgs& p, f32x16 (&acc)[C::FM][C::FN], int row0,
+                                             int col0, int lane) {
+  const int half = lane >> 5, l = lane & 31;
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) {
+    const int m = row0 + 32 * i + l;
+    int id = m < p.M ? p.adapter[m] : -1;
+    id = id < p.adapters ? id : -1;
+    unsigned left = static_cast<unsigned>(__ballot(id >= 0));  // lanes 32.. repeat these rows
+    if (left == 0) continue;
+    int own[16];  // adapters of the accumulators' rows
+#pragma unroll
+    for (int e = 0; e < 16; ++e) own[e] = __shfl(id, 8 * (e >> 2) + 4 * half + (e & 3));
+    const uint16_t* h = p.h + static_cast<int64_t>(min(m, p.M - 1)) * (2 * p.pad) + 8 * half;
+    do {
+      const int g = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+      left &= ~static_cast<unsigned>(__ballot(id == g));
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) {
+        const int n = min(col0 + 32 * j + l, p.N - 1);
+        const uint16_t* u = p.up + g * p.stride_up + n * p.ld_up;
+        f32x16 d;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) d[e] = 0.f;
+        for (int t = 0; t < p.pad; t += 16) {
+          // Columns past the rank are zeros in h, and have to be here too: what
+          // lies there belongs to another row.
+          const int r = t + 8 * half;
+          i32x4 b = {0, 0, 0, 0};
+          if (p.up_vec) {
+            if (r < p.rank) b = *reinterpret_cast<const i32x4*>(u + r);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (r + q < p.rank) b[q >> 1] |= static_cast<int>(static_cast<uint32_t>(u[r + q]) << (16 * (q & 1)));
+          }
+          const bf16x8 bu = __builtin_bit_cast(bf16x8, b);
+          d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(h + t), bu, d, 0, 0, 0);
+          d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(h + p.pad + t), bu, d, 0, 0, 0);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] += own[e] == g ? d[e] : 0.f;
+      }
+    } while (left != 0);
+  }
+}
+
 // ------------------------------------------------------------------- the kernel
+
+template <int MODE>
+using ArgsOf = std::conditional_t<MODE == MODE_LORA, LoraArgs, GemmArgs>;
 
 // RAGGED: K may end inside a 16-byte chunk of a DMA-fed row (patch_tail).
 // Kept out of the other instantiations: the patch's code perturbs the
 // register allocation of the K loop.
 template <class C, int LA, int LB, int OUT, bool SPLIT, bool RAGGED, int MODE = MODE_DENSE>
 __global__ void __launch_bounds__(C::NT)
-gemm_tile_kernel(GemmArgs p) {
+gemm_tile_kernel(ArgsOf<MODE> p) {
   // The LDS block holds the ring of K slices, and after the main loop the
   // epilogue's staging strips.
   constexpr int RING = C::KG * C::STAGES * C::STAGE;
@@ -685,7 +747,7 @@ gemm_tile_kernel(GemmArgs p) {
 
   // ---- which tile and which K range
   int tm, tn, split = 0;
-  if constexpr (MODE == MODE_DENSE) {
+  if constexpr (MODE == MODE_DENSE || MODE == MODE_LORA) {
     const int tiles = p.tiles_m * p.tiles_n;
     const int L = xcd_remap(blockIdx.x, gridDim.x);
     split = L / tiles;
@@ -1244,6 +1306,10 @@ gemm_tile_kernel(GemmArgs p) {
   }
   float* elds = reinterpret_cast<float*>(smem + wave * EpiLayout<C>::WAVE_BYTES);
   const int row0 = m0 + wm0, col0 = n0 + wn0;
+  if constexpr (MODE == MODE_LORA) {
+    // (Without adapters there are no arrays of them to read.)
+    if (p.adapters > 0 && (!SPLIT || split == 0)) add_adapters<C>(p, acc, row0, col0, lane);
+  }
   run_epilogue<C, OUT, SPLIT>(p, acc, elds, row0, col0, lane, split);
 }
 
@@ -1347,9 +1413,10 @@ __global__ void __launch_bounds__(256) splitk_reduce4_kernel(GemmArgs p) {
 // This file is compiled once per (ragged, output part) pair, with G355_PART
 // (an OutPart) and G355_RAGGED (0 or 1) defined, and once with G355_REDUCE
 // for the split-K reduction: each compile instantiates only the kernels of its
-// output kind, so the kernel variants build in parallel. G355_I8, G355_GROUPED
-// and G355_WGRAD select the INT8 kernels, the grouped products and their
-// weight gradient instead of the dense BF16 and FP8 kernels.
+// output kind, so the kernel variants build in parallel. G355_I8, G355_GROUPED,
+// G355_WGRAD and G355_LORA select the INT8 kernels, the grouped products, their
+// weight gradient and the product with adapters instead of the dense BF16 and
+// FP8 kernels.
 #if defined(G355_PART)
 
 constexpr int PART = G355_PART;
@@ -1508,6 +1575,25 @@ hipError_t G355_WGRAD_LAUNCHER(G355_PART)(const GroupedPlan& plan, const LaunchS
   return launch_grouped<Small16, LOAD_ROWS, LOAD_ROWS, false, MODE_WGRAD>(plan.grid, a, stream);
 }
 
+#elif defined(G355_LORA)
+
+template <class C>
+static hipError_t launch_lora_cfg(const Plan& plan, const LoraArgs& a, hipStream_t stream) {
+  constexpr int OUT = PART == PART_BF16 ? OUT_BF16 : OUT_F32;
+  hipLaunchKernelGGL((gemm_tile_kernel<C, LOAD_DIRECT, LOAD_DIRECT, OUT, PART == PART_SPLIT,
+                                       G355_RAGGED != 0, MODE_LORA>),
+                     dim3(static_cast<unsigned>(plan.grid)), dim3(C::NT), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t G355_LORA_LAUNCHER(G355_RAGGED, G355_PART)(const Plan& plan, const LoraArgs& a, hipStream_t stream) {
+  if (plan.bm == 64)
+    return plan.bn == 256 ? launch_lora_cfg<Thin16>(plan, a, stream) : launch_lora_cfg<Narrow16>(plan, a, stream);
+  if (plan.bm == 256 && plan.bn == 256) return launch_lora_cfg<Big16>(plan, a, stream);
+  if (plan.bm == 256) return launch_lora_cfg<Mid16>(plan, a, stream);
+  return launch_lora_cfg<Small16>(plan, a, stream);
+}
+
 #else
 
 // The launches of launch_tile, with the kernels' RAGGED flag R. Register
@@ -1579,7 +1665,7 @@ hipError_t G355_PART_LAUNCHER(G355_RAGGED, G355_PART)(const Plan& plan, const La
   return launch_tile_t<G355_RAGGED != 0>(plan, spec, args, stream);
 }
 
-#endif  // G355_I8 / G355_GROUPED / G355_WGRAD / dense
+#endif  // G355_I8 / G355_GROUPED / G355_WGRAD / G355_LORA / dense
 
 #elif defined(G355_REDUCE)
 

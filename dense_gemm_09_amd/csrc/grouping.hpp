@@ -15,7 +15,8 @@ constexpr int kBufferWord3 = 0x00020000;
 // MODE_GROUPED: rows offsets[g] .. offsets[g+1]-1 of A and C belong to group
 // g, which has a B (bias, scale_b, sum_b) of its own. MODE_WGRAD: C of group g
 // is the product of two operands over those rows (their contraction axis).
-enum TileMode : int { MODE_DENSE = 0, MODE_GROUPED = 1, MODE_WGRAD = 2 };
+// MODE_LORA: a dense product to which each row's low-rank adapter is added.
+enum TileMode : int { MODE_DENSE = 0, MODE_GROUPED = 1, MODE_WGRAD = 2, MODE_LORA = 3 };
 
 // Tile rows that a group's tiles are numbered along before the next column: the
 // tiles in flight on an XCD share that many row panels, and a group of that many

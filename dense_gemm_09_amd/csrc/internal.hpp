@@ -33,6 +33,8 @@ struct Plan {
 
 // Chooses the kernel, tile and split for a shape (host arithmetic only).
 Plan make_plan(int64_t M, int64_t N, int64_t K, bool fp8);
+// The same among the tile kernels alone.
+Plan make_tile_plan(int64_t M, int64_t N, int64_t K, bool fp8);
 
 // Largest K of an INT8 product: K * 128 * 128 stays inside INT32.
 constexpr int64_t kMaxInt8K = 131071;
@@ -90,6 +92,17 @@ G355_DECLARE_GROUPED(G355_GROUPED_LAUNCHER(0, 1)) G355_DECLARE_GROUPED(G355_GROU
 G355_DECLARE_GROUPED(G355_GROUPED_LAUNCHER(1, 1)) G355_DECLARE_GROUPED(G355_GROUPED_LAUNCHER(1, 2))
 G355_DECLARE_GROUPED(G355_WGRAD_LAUNCHER(1)) G355_DECLARE_GROUPED(G355_WGRAD_LAUNCHER(2))
 #undef G355_DECLARE_GROUPED
+
+// The projection with low-rank adapters: BF16 operands by DMA, FP32 and BF16
+// output and split-K partials.
+struct LoraArgs;  // lora.hpp
+#define G355_LORA_LAUNCHER_(r, p) launch_lora_r##r##_p##p
+#define G355_LORA_LAUNCHER(r, p) G355_LORA_LAUNCHER_(r, p)
+#define G355_DECLARE_LORA(r, p)                                                              \
+  hipError_t G355_LORA_LAUNCHER(r, p)(const Plan& plan, const LoraArgs& args, hipStream_t stream);
+G355_DECLARE_LORA(0, 0) G355_DECLARE_LORA(0, 1) G355_DECLARE_LORA(0, 2)
+G355_DECLARE_LORA(1, 0) G355_DECLARE_LORA(1, 1) G355_DECLARE_LORA(1, 2)
+#undef G355_DECLARE_LORA
 
 // 256x256 tiles with FP32 or BF16 output (gemm_turn.hip), one element type
 // each: grouped products (INT8: the dense one too, where groups is 0) and the

@@ -1,0 +1,140 @@
+// C ABI of the projection with low-rank adapters: argument validation, plan and dispatch.
+//
+// Two launches (three with a split K): the first factors' product h, and the
+// projection's own kernel, which adds h times the second factors to its
+// accumulators before its epilogue.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "gemm355.h"
+#include "internal.hpp"
+#include "lora.hpp"
+
+using namespace g355;
+
+namespace {
+
+constexpr int64_t kMaxDim = int64_t{1} << 30;
+constexpr int64_t k2G = int64_t{1} << 31;
+
+bool bad_dim(int64_t v) { return v < 0 || v > kMaxDim; }
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Bytes of h, in front of the partial sums of a split K.
+size_t h_bytes(int64_t M, int64_t R) {
+  return (static_cast<size_t>(M) * 4 * padded_rank(R) + 255) / 256 * 256;
+}
+
+}  // namespace
+
+hipError_t g355::launch_lora(const Plan& plan, const LaunchSpec& spec, const LoraArgs& args, hipStream_t stream) {
+  using Fn = hipError_t (*)(const Plan&, const LoraArgs&, hipStream_t);
+  static constexpr Fn kParts[2][3] = {{launch_lora_r0_p0, launch_lora_r0_p1, launch_lora_r0_p2},
+                                      {launch_lora_r1_p0, launch_lora_r1_p1, launch_lora_r1_p2}};
+  const int part = plan.split > 1 ? PART_SPLIT : spec.out == OUT_F32 ? PART_F32 : PART_BF16;
+  return kParts[spec.ragged ? 1 : 0][part](plan, args, stream);
+}
+
+extern "C" {
+
+size_t gemm_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t R) {
+  if (M <= 0 || N <= 0 || bad_dim(M) || bad_dim(N) || bad_dim(K) || R < 0 || R > kMaxRank) return 0;
+  return h_bytes(M, R) + make_tile_plan(M, N, K, false).workspace;
+}
+
+gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R, float alpha,
+                           const void* A, int64_t lda, const void* B, int64_t ldb,
+                           const int32_t* adapter, const void* down, int64_t ld_down,
+                           int64_t stride_down, const void* up, int64_t ld_up, int64_t stride_up,
+                           const float* scale, float beta, void* C, int64_t ldc,
+                           gemm_out_dtype c_dtype, const void* bias, gemm_act act,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if ((c_dtype != GEMM_OUT_F32 && c_dtype != GEMM_OUT_BF16) || act < GEMM_ACT_NONE ||
+      act > GEMM_ACT_GELU_TANH)
+    return GEMM_ERR_BAD_ENUM;
+  if (bad_dim(M) || bad_dim(N) || bad_dim(K) || G < 0 || R < 0) return GEMM_ERR_BAD_DIM;
+  if (R > kMaxRank || G > kMaxAdapters) return GEMM_ERR_UNSUPPORTED;
+  const bool adapters = G > 0 && R > 0;
+  if (lda < std::max<int64_t>(1, K) || ldb < std::max<int64_t>(1, K) || ldc < std::max<int64_t>(1, N))
+    return GEMM_ERR_BAD_LD;
+  if (adapters && (ld_down < std::max<int64_t>(1, K) || ld_up < R || stride_down < 0 || stride_up < 0))
+    return GEMM_ERR_BAD_LD;
+  if (M == 0 || N == 0) return GEMM_OK;
+  if (C == nullptr || (K > 0 && (A == nullptr || B == nullptr))) return GEMM_ERR_NULL_POINTER;
+  if (adapters && (adapter == nullptr || up == nullptr || (K > 0 && down == nullptr)))
+    return GEMM_ERR_NULL_POINTER;
+  const size_t need = gemm_lora_workspace_size(M, N, K, R);
+  if (need > 0 && workspace == nullptr) return GEMM_ERR_NULL_POINTER;
+  if (workspace_bytes < need) return GEMM_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(workspace, 16) || !aligned(adapter, 4) || !aligned(scale, 4) || !aligned(down, 2) ||
+      !aligned(up, 2) || !aligned(A, 2) || !aligned(B, 2) || !aligned(bias, 2) ||
+      !aligned(C, c_dtype == GEMM_OUT_F32 ? 4 : 2))
+    return GEMM_ERR_UNSUPPORTED;
+  // The copies' 32-bit offsets.
+  if (((M - 1) * lda + K) * 2 >= k2G || ((N - 1) * ldb + K) * 2 >= k2G) return GEMM_ERR_UNSUPPORTED;
+
+  const Plan plan = make_tile_plan(M, N, K, false);
+  if (plan.grid > INT32_MAX) return GEMM_ERR_BAD_DIM;
+  const auto s = static_cast<hipStream_t>(stream);
+  LoraArgs a{};
+  a.A = A;
+  a.B = B;
+  a.C = C;
+  a.bias = static_cast<const uint16_t*>(bias);
+  a.workspace = reinterpret_cast<float*>(static_cast<char*>(workspace) + h_bytes(M, R));
+  a.lda = lda;
+  a.ldb = ldb;
+  a.ldc = ldc;
+  a.M = static_cast<int>(M);
+  a.N = static_cast<int>(N);
+  a.K = static_cast<int>(K);
+  a.alpha = alpha;
+  a.beta = beta;
+  a.act = act;
+  a.c_vec = aligned(C, c_dtype == GEMM_OUT_F32 ? 16 : 8) && ldc % 4 == 0 ? 1 : 0;
+  a.ws_vec = 1;
+  a.split_k = plan.split;
+  a.k_split_len = plan.k_split_len;
+  a.tiles_m = static_cast<int>((M + plan.bm - 1) / plan.bm);
+  a.tiles_n = static_cast<int>((N + plan.bn - 1) / plan.bn);
+  a.adapter = adapter;
+  a.h = static_cast<uint16_t*>(workspace);
+  a.up = static_cast<const uint16_t*>(up);
+  a.ld_up = ld_up;
+  a.stride_up = stride_up;
+  a.adapters = adapters ? static_cast<int>(G) : 0;
+  a.rank = static_cast<int>(R);
+  a.pad = static_cast<int>(padded_rank(R));
+  a.up_vec = R % 8 == 0 && ld_up % 8 == 0 && stride_up % 8 == 0 && aligned(up, 16) ? 1 : 0;
+  (void)hipGetLastError();  // an earlier call's pending error is not this call's
+  if (adapters) {
+    LoraDownArgs d{};
+    d.A = static_cast<const uint16_t*>(A);
+    d.lda = lda;
+    d.adapter = adapter;
+    d.down = static_cast<const uint16_t*>(down);
+    d.ld_down = ld_down;
+    d.stride_down = stride_down;
+    d.scale = scale;
+    d.h = a.h;
+    d.M = a.M;
+    d.K = a.K;
+    d.adapters = a.adapters;
+    d.rank = a.rank;
+    d.pad = a.pad;
+    if (launch_lora_down(d, s) != hipSuccess) return GEMM_ERR_HIP;
+  }
+  LaunchSpec spec{};
+  spec.a_kmajor = spec.b_kmajor = true;
+  spec.loader_a = spec.loader_b = LOAD_DIRECT;
+  spec.out = c_dtype == GEMM_OUT_F32 ? OUT_F32 : OUT_BF16;
+  spec.ragged = K % 8 != 0;
+  if (launch_lora(plan, spec, a, s) != hipSuccess) return GEMM_ERR_HIP;
+  if (plan.split > 1 && launch_splitk_reduce(plan, spec, a, s) != hipSuccess) return GEMM_ERR_HIP;
+  return GEMM_OK;
+}
+
+}  // extern "C"

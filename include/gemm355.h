@@ -376,6 +376,159 @@ gemm_status gemm_grouped_bf16_wgrad(int64_t G, int64_t T, int64_t N, int64_t K, 
                                     int64_t stride_c, gemm_out_dtype c_dtype, void* stream);
 
 /*
+ * Routing: which experts a token's rows go to, and with what weights.
+ * For every token t, from its logits x[t, e] (e < E):
+ *
+ *   s_e = softmax over e of x[t, e], or sigmoid(x[t, e])
+ *   c_e = s_e + bias[e]                          (bias chooses, it is in no weight)
+ *   groups > 1: E/groups neighbouring experts are a group; a group's score is the
+ *     sum of its group_best (1 or 2) largest c; only experts of the top_groups
+ *     best groups are chosen
+ *   expert[t, 0..top_k-1] = the experts of the top_k largest c, largest first
+ *   weight[t, j] = scale * s_j, or scale * s_j / sum over the chosen s (renormalise != 0)
+ *
+ * Equal values go to the lowest index, of experts as of groups. The choice is
+ * that of exact arithmetic: without bias (and with one best per group) it
+ * compares the logits themselves, otherwise scores in 64 bits. Weights are
+ * FP32; renormalised ones are formed from the scores' logarithms, so that
+ * scores too small for FP32 still have shares.
+ * An expert whose logit (or bias) is -inf is not available. A token with fewer
+ * than top_k available experts (in its groups) has expert -1 and weight 0 in
+ * the slots that are left: a row that is all -inf, such as padding, in all of
+ * them. A row with a NaN (under softmax: or +inf) has expert -1 and weight
+ * NaN. A NaN in bias makes its expert unavailable.
+ * logits: T rows of E, FP32 or BF16 (l_dtype), ldl >= E. bias: FP32[E] or
+ * NULL. expert: INT32[T][top_k]; weight: FP32[T][top_k]; contiguous.
+ * E at most 1024, top_k at most 32 and groups at most 64 (else
+ * GEMM_ERR_UNSUPPORTED). GEMM_ERR_BAD_DIM: T negative or above 2^30, E < 1,
+ * groups that do not divide E, top_groups outside [1, groups], group_best other
+ * than 1 or 2, top_k < 1 or above the experts of top_groups groups.
+ * GEMM_ERR_BAD_ENUM: l_dtype, score. Then GEMM_ERR_BAD_LD,
+ * GEMM_ERR_NULL_POINTER, GEMM_ERR_HIP. T == 0 launches nothing.
+ */
+typedef enum { GEMM_SCORE_SOFTMAX = 0, GEMM_SCORE_SIGMOID = 1 } gemm_score;
+
+gemm_status gemm_route(int64_t T, int64_t E, int64_t top_k, const void* logits, int64_t ldl,
+                       gemm_out_dtype l_dtype, gemm_score score, const float* bias,
+                       int64_t groups, int64_t top_groups, int group_best, int renormalise,
+                       float scale, int32_t* expert, float* weight, void* stream);
+
+/*
+ * Gradient of gemm_route's weights with respect to its logits, the choice held
+ * fixed: dlogits[t, e] = sum_j dweight[t, j] * d weight[t, j] / d x[t, e], for
+ * all E columns (zeros where nothing arrives), in the logits' type, FP32
+ * before its one rounding. The bias has no gradient.
+ * expert as gemm_route wrote it; slots whose expert is outside [0, E) are
+ * passed over, and their dweight is not used. A row without any expert gets
+ * zeros. An expert named by several slots gets the sum of their gradients.
+ * dlogits: T rows of E, ldd >= E; may not overlap the inputs. Limits and
+ * errors as for gemm_route.
+ */
+gemm_status gemm_route_grad(int64_t T, int64_t E, int64_t top_k, const void* logits, int64_t ldl,
+                            gemm_out_dtype l_dtype, gemm_score score, int renormalise, float scale,
+                            const int32_t* expert, const float* dweight, void* dlogits,
+                            int64_t ldd, void* stream);
+
+/*
+ * The order of rows by expert: S slots (S = T * top_k, slot t * top_k + j) with
+ * an expert each are sorted by expert, stably, into rows.
+ *   offsets[g]  = slots whose expert is below g: the offsets of the grouped
+ *                 products, G + 1 of them; offsets[G] slots have an expert
+ *   position[s] = the row of slot s, or -1 if its expert is outside [0, G)
+ *   order[r]    = the slot of row r, or -1 for the rows from offsets[G] on
+ * expert, position: INT32[S]; offsets: INT32[G+1]; order: INT32[S] or NULL.
+ * No array may overlap another. Nothing is synchronised.
+ * workspace: device scratch of gemm_route_order_workspace_size(S, G) bytes,
+ * 4-byte aligned. G at most 8192 (GEMM_ERR_UNSUPPORTED). GEMM_ERR_BAD_DIM: S
+ * negative or above 2^30, G < 0. S == 0 writes zeros to offsets.
+ */
+gemm_status gemm_route_order(int64_t S, int64_t G, const int32_t* expert, int32_t* offsets,
+                             int32_t* position, int32_t* order, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of gemm_route_order; 0 for sizes it refuses. */
+size_t gemm_route_order_workspace_size(int64_t S, int64_t G);
+
+/*
+ * Rows of tokens to their experts: Y[position[t * top_k + j], :] = X[t, :]
+ * X: T rows of N elements of elem_bytes (1, 2 or 4: codes, BF16, FP32 or the
+ * scales of codes; moved as bits), ldx >= N. Y: R rows, ldy >= N. Positions
+ * outside [0, R) are passed over. Rows of Y that no slot names are not
+ * written. A position named twice gets one of its rows.
+ * Its gradient is gemm_combine_rows without weights.
+ * Errors: GEMM_ERR_BAD_ENUM (elem_bytes), GEMM_ERR_BAD_DIM (a size negative or
+ * above 2^30, T * top_k above 2^30, top_k < 1), GEMM_ERR_UNSUPPORTED (top_k above 64, X or Y not
+ * aligned to its elements), GEMM_ERR_BAD_LD,
+ * GEMM_ERR_NULL_POINTER, GEMM_ERR_HIP. T == 0, R == 0 or N == 0 launches nothing.
+ */
+gemm_status gemm_dispatch_rows(int64_t T, int64_t top_k, int64_t R, int64_t N, const void* X,
+                               int64_t ldx, int elem_bytes, const int32_t* position, void* Y,
+                               int64_t ldy, void* stream);
+
+/*
+ * Rows of experts back to their tokens:
+ *   C[t, :] = sum_j weight[t, j] * Y[position[t * top_k + j], :] + beta * C[t, :]
+ * summed in FP32 in the order of j, rounded once. Slots with a position
+ * outside [0, R) add nothing, whatever their weight (a token without slots:
+ * beta * C). Y: R rows of N, FP32 or BF16, ldy >= N. weight: FP32[T][top_k],
+ * or NULL for ones. C: T rows, FP32 or BF16, ldc >= N, not read for beta == 0.
+ * Errors as for gemm_dispatch_rows; GEMM_ERR_BAD_ENUM for the types. T == 0 or
+ * N == 0 launches nothing; R == 0 gives beta * C.
+ */
+gemm_status gemm_combine_rows(int64_t T, int64_t top_k, int64_t R, int64_t N, const void* Y,
+                              int64_t ldy, gemm_out_dtype y_dtype, const int32_t* position,
+                              const float* weight, float beta, void* C, int64_t ldc,
+                              gemm_out_dtype c_dtype, void* stream);
+
+/*
+ * Gradients of gemm_combine_rows, D being C's:
+ *   dY[position[t * top_k + j], :] = weight[t, j] * D[t, :]
+ *   dweight[t, j] = sum over n of D[t, n] * Y[position[t * top_k + j], n]   (0 without a position)
+ * D: T rows of N, d_dtype, ldd >= N. Y, dY: R rows, y_dtype. weight as above
+ * (NULL: ones). dweight: FP32[T][top_k], or NULL: it is not computed and Y,
+ * which may be NULL then, not read. Rows of dY that no slot names are not
+ * written. dY may not overlap Y. Sums are FP32. Errors as above.
+ */
+gemm_status gemm_combine_rows_grad(int64_t T, int64_t top_k, int64_t R, int64_t N, const void* D,
+                                   int64_t ldd, gemm_out_dtype d_dtype, const void* Y, int64_t ldy,
+                                   gemm_out_dtype y_dtype, const int32_t* position,
+                                   const float* weight, void* dY, int64_t lddy, float* dweight,
+                                   void* stream);
+
+/*
+ * A shared projection with low-rank adapters, of many requests at once: row m
+ * of A belongs to a request that has adapter a = adapter[m] of its own,
+ *
+ *   C[m,:] = act( alpha * (A[m,:] B + scale[a] * (A[m,:] down_a) up_a) + beta * C[m,:] + bias )
+ *
+ * and the plain projection where adapter[m] is outside [0, G). Rows come in
+ * any order; neighbours that share an adapter share its work.
+ * A: BF16, M rows of K (ROW), lda >= K. B: BF16, N rows of K (COL: K-major;
+ * gemm_pack_b reorders a weight), ldb >= K. adapter: INT32[M].
+ * down: BF16, adapter g's R rows of K start stride_down * g elements in,
+ * ld_down >= K. up: BF16, its N rows of R at stride_up * g, ld_up >= R.
+ * (An adapter of lower rank has rows of zeros in down.) scale: FP32[G], or
+ * NULL for ones. R at most 128; G == 0 or R == 0 is the plain projection.
+ * Sums are FP32. scale * (A down) passes to the second product as two BF16
+ * values that together keep 16 bits of it. An adapter's infinities and NaN
+ * stay in its own rows. C, bias, act, beta and alpha as in gemm_bf16.
+ * workspace: gemm_lora_workspace_size(M, N, K, R) bytes, 16-byte aligned.
+ * Errors as for gemm_bf16; GEMM_ERR_BAD_LD also for a negative stride_down or
+ * stride_up; GEMM_ERR_UNSUPPORTED for R above 128 or G above 65536, A or B that spans
+ * 2^31 bytes or more, BF16 operands at odd addresses, a workspace not 16-byte aligned.
+ */
+gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R, float alpha,
+                           const void* A, int64_t lda, const void* B, int64_t ldb,
+                           const int32_t* adapter, const void* down, int64_t ld_down,
+                           int64_t stride_down, const void* up, int64_t ld_up, int64_t stride_up,
+                           const float* scale, float beta, void* C, int64_t ldc,
+                           gemm_out_dtype c_dtype, const void* bias, gemm_act act,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of gemm_lora_bf16; 0 for sizes it refuses. */
+size_t gemm_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t R);
+
+/*
  * One-time reorder of a weight matrix B (logical K x N) into the layout the
  * fast path reads: Bp[n*ldbp + k] = b(k, n), i.e. GEMM_COL_MAJOR (K-major)
  * with leading dimension ldbp. The FP8 DeepGEMM page (sec. 3.2) rearranges B
