@@ -292,41 +292,106 @@ hipError_t launch_route_grad(const RouteGradArgs& a, bool bf16, hipStream_t stre
 
 // ------------------------------------------------------------- order of rows
 
-// A stable counting sort in three launches: every wave counts the experts of
-// its chunk of slots; one workgroup turns the counts into each chunk's first
-// row of each expert; every wave places its chunk. Slots without an expert are
-// an expert G behind the others. No result depends on the order of atomics:
-// those that are there add up integers.
+// A stable counting sort. Slots are divided into chunks, chunks into a segment
+// for each wave of a workgroup. Up to kSmallSlots slots are one chunk and one
+// launch; otherwise a first launch counts every chunk's experts, and in the
+// second every workgroup adds up the counts of the chunks (there are at most
+// kMaxChunks), which gives the first row of each expert in its chunk, and places
+// its slots. Slots without an expert are an expert G behind the others. Within a
+// wave, slots of one expert find each other by ballots over the expert's bits, 64
+// at a time. The only atomics add up integers: no result depends on their order.
+//
+// All of it is latency: a second launch costs more than what it does (32768 slots of 64
+// experts: three launches with a scan of their own took 15 us).
 
-constexpr int kScanThreads = 1024;
+constexpr int kSmallWaves = 16;      // 512 slots a wave, eight to a lane
+constexpr int kOrderWaves = 4;
+constexpr int kHeldKeys = 8;         // keys that a lane holds at a time
+constexpr int kMaxChunks = 128;
 
 __device__ __forceinline__ int expert_key(const OrderArgs& p, int s) {
   const int e = p.expert[s];
   return e >= 0 && e < p.G ? e : p.G;
 }
 
-__global__ void __launch_bounds__(64) order_count_kernel(OrderArgs p) {
-  extern __shared__ int counter[];
-  const int lane = threadIdx.x;
-  for (int g = lane; g <= p.G; g += 64) counter[g] = 0;
-  __syncthreads();
-  const int end = min(p.S, (static_cast<int>(blockIdx.x) + 1) * p.chunk);
-  for (int s = blockIdx.x * p.chunk + lane; s < end; s += 64) atomicAdd(&counter[expert_key(p, s)], 1);
-  __syncthreads();
-  int32_t* out = p.counts + static_cast<int64_t>(blockIdx.x) * (p.G + 1);
-  for (int g = lane; g <= p.G; g += 64) out[g] = counter[g];
+// Keys of slots s0 + 64 h + lane below `end` (-1 past it).
+__device__ __forceinline__ void load_keys(const OrderArgs& p, int s0, int end, int lane, int (&key)[kHeldKeys]) {
+#pragma unroll
+  for (int h = 0; h < kHeldKeys; ++h) {
+    const int s = s0 + 64 * h + lane;
+    key[h] = s < end ? expert_key(p, s) : -1;
+  }
 }
 
-__global__ void __launch_bounds__(kScanThreads) order_scan_kernel(OrderArgs p) {
-  __shared__ int part[kScanThreads / 64];
+// Counts the experts of slots [begin, end) in a wave's counters.
+__device__ __forceinline__ void count_keys(const OrderArgs& p, int begin, int end, int lane, int* counter) {
+  for (int s0 = begin; s0 < end; s0 += 64 * kHeldKeys) {
+    int key[kHeldKeys];
+    load_keys(p, s0, end, lane, key);
+#pragma unroll
+    for (int h = 0; h < kHeldKeys; ++h)
+      if (key[h] >= 0) atomicAdd(&counter[key[h]], 1);
+  }
+}
+
+// LDS of this wave as its other lanes have left it.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+__global__ void __launch_bounds__(64 * kOrderWaves) order_count_kernel(OrderArgs p) {
+  extern __shared__ int counter[];
+  for (int g = threadIdx.x; g <= p.G; g += 64 * kOrderWaves) counter[g] = 0;
+  __syncthreads();
+  const int begin = blockIdx.x * p.chunk, end = min(p.S, begin + p.chunk);
+  const int seg = p.chunk / kOrderWaves;  // a multiple of 64
+  const int wave = threadIdx.x >> 6, from = begin + wave * seg;
+  count_keys(p, from, min(end, from + seg), threadIdx.x & 63, counter);
+  __syncthreads();
+  int32_t* out = p.counts + static_cast<int64_t>(blockIdx.x) * (p.G + 1);
+  for (int g = threadIdx.x; g <= p.G; g += 64 * kOrderWaves) out[g] = counter[g];
+}
+
+// WAVES counters of G + 1 experts in LDS. SMALL: the only workgroup.
+template <int WAVES, bool SMALL>
+__global__ void __launch_bounds__(64 * WAVES) order_place_kernel(OrderArgs p) {
+  extern __shared__ int counter[];
+  __shared__ int part[WAVES];
+  constexpr int NT = 64 * WAVES;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int bins = p.G + 1;
+  const int chunk = static_cast<int>(blockIdx.x);
+  const int begin = chunk * p.chunk, end = min(p.S, begin + p.chunk);
+  const int seg = p.chunk / WAVES;
+  const int from = begin + wave * seg, to = min(end, from + seg);
+
+  for (int i = tid; i < WAVES * bins; i += NT) counter[i] = 0;
+  __syncthreads();
+  int* mine = counter + wave * bins;
+  count_keys(p, from, to, lane, mine);
+  __syncthreads();
+
+  // Counters become first rows: of the experts in order, in each the chunks
+  // before this one, in that the waves.
   int carry = 0;  // rows of the experts before this round's
-  for (int g0 = 0; g0 < bins; g0 += kScanThreads) {
+  for (int g0 = 0; g0 < bins; g0 += NT) {
     const int g = g0 + tid;
-    int total = 0;
-    if (g < bins)
-      for (int c = 0; c < p.chunks; ++c) total += p.counts[static_cast<int64_t>(c) * bins + g];
+    int total = 0, before = 0;
+    if (g < bins) {
+      if constexpr (SMALL) {
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) total += counter[w * bins + g];
+      } else {
+#pragma unroll 8
+        for (int c = 0; c < p.chunks; ++c) {
+          const int n = p.counts[static_cast<int64_t>(c) * bins + g];
+          total += n;
+          before += c < chunk ? n : 0;
+        }
+      }
+    }
     int incl = total;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -335,76 +400,80 @@ __global__ void __launch_bounds__(kScanThreads) order_scan_kernel(OrderArgs p) {
     }
     if (lane == 63) part[wave] = incl;
     __syncthreads();
-    int before = carry, all = 0;
-    for (int w = 0; w < kScanThreads / 64; ++w) {
-      before += w < wave ? part[w] : 0;
-      all += part[w];
+    int row = carry + incl - total;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      row += w < wave ? part[w] : 0;
+      carry += part[w];
     }
-    int row = before + incl - total;
     if (g < bins) {
-      p.offsets[g] = row;
-      for (int c = 0; c < p.chunks; ++c) {
-        int32_t* n = p.counts + static_cast<int64_t>(c) * bins + g;
-        const int here = *n;
-        *n = row;
-        row += here;
+      if (chunk == 0) p.offsets[g] = row;
+      row += before;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        const int n = counter[w * bins + g];
+        counter[w * bins + g] = row;
+        row += n;
       }
     }
-    carry += all;
     __syncthreads();
   }
-}
 
-__global__ void __launch_bounds__(64) order_place_kernel(OrderArgs p) {
-  extern __shared__ int counter[];
-  const int lane = threadIdx.x;
-  const int32_t* in = p.counts + static_cast<int64_t>(blockIdx.x) * (p.G + 1);
-  for (int g = lane; g <= p.G; g += 64) counter[g] = in[g];
-  __syncthreads();
   int bits = 0;
   while ((p.G >> bits) != 0) ++bits;
-  const int end = min(p.S, (static_cast<int>(blockIdx.x) + 1) * p.chunk);
-  for (int s0 = blockIdx.x * p.chunk; s0 < end; s0 += 64) {
-    const int s = s0 + lane;
-    const bool in_range = s < end;
-    const int key = in_range ? expert_key(p, s) : 0;
-    // Lanes with the same expert.
-    unsigned long long same = __ballot(in_range);
-    for (int b = 0; b < bits; ++b) {
-      const bool set = (key >> b) & 1;
-      const unsigned long long with = __ballot(set);
-      same &= set ? with : ~with;
+  for (int s0 = from; s0 < to; s0 += 64 * kHeldKeys) {
+    int key[kHeldKeys];
+    load_keys(p, s0, to, lane, key);
+#pragma unroll
+    for (int h = 0; h < kHeldKeys; ++h) {
+      const int s = s0 + 64 * h + lane;
+      const bool in_range = key[h] >= 0;
+      unsigned long long same = __ballot(in_range);  // lanes with the same expert
+      if (same == 0) break;
+      for (int b = 0; b < bits; ++b) {
+        const bool set = (key[h] >> b) & 1;
+        const unsigned long long with = __ballot(set);
+        same &= set ? with : ~with;
+      }
+      int first = 0;
+      if (in_range) first = mine[key[h]];
+      wave_fence();
+      if (in_range) {
+        // The last of them moves the counter on.
+        if ((same >> lane) == 1) mine[key[h]] = first + __popcll(same);
+        const int row = first + __popcll(same & ((1ull << lane) - 1));
+        const bool live = key[h] < p.G;
+        p.position[s] = live ? row : -1;
+        if (p.order) p.order[row] = live ? s : -1;
+      }
+      wave_fence();
     }
-    if (in_range) {
-      const int row = counter[key] + __popcll(same & ((1ull << lane) - 1));
-      const bool live = key < p.G;
-      p.position[s] = live ? row : -1;
-      if (p.order) p.order[row] = live ? s : -1;
-    }
-    __syncthreads();  // every lane has read its counter
-    if (in_range && (same >> lane) == 1) counter[key] += __popcll(same);
-    __syncthreads();
   }
 }
 
-void order_chunks(int64_t S, int& chunk, int& chunks) {
-  // At most 1024 chunks, of 512 slots or more.
-  const int64_t per = (S + 1023) / 1024;
-  chunk = static_cast<int>(per <= 512 ? 512 : (per + 63) / 64 * 64);
+void order_chunks(int64_t S, int64_t G, int& chunk, int& chunks) {
+  if (order_small(S, G)) {
+    chunk = static_cast<int>((S + 64 * kSmallWaves - 1) / (64 * kSmallWaves) * (64 * kSmallWaves));
+    chunks = 1;
+    return;
+  }
+  const int64_t least = 64 * kHeldKeys * kOrderWaves, per = (S + kMaxChunks - 1) / kMaxChunks;
+  chunk = static_cast<int>((per + least - 1) / least * least);
   chunks = static_cast<int>((S + chunk - 1) / chunk);
 }
 
 hipError_t launch_order(const OrderArgs& a, hipStream_t stream) {
   const size_t lds = static_cast<size_t>(a.G + 1) * sizeof(int);
-  if (a.chunks > 0) {
-    hipLaunchKernelGGL(order_count_kernel, dim3(a.chunks), dim3(64), lds, stream, a);
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
+  if (order_small(a.S, a.G)) {
+    hipLaunchKernelGGL((order_place_kernel<kSmallWaves, true>), dim3(1), dim3(64 * kSmallWaves), kSmallWaves * lds,
+                       stream, a);
+    return hipGetLastError();
   }
-  hipLaunchKernelGGL(order_scan_kernel, dim3(1), dim3(kScanThreads), 0, stream, a);
+  hipLaunchKernelGGL(order_count_kernel, dim3(a.chunks), dim3(64 * kOrderWaves), lds, stream, a);
   const hipError_t err = hipGetLastError();
-  if (err != hipSuccess || a.chunks == 0) return err;
-  hipLaunchKernelGGL(order_place_kernel, dim3(a.chunks), dim3(64), lds, stream, a);
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL((order_place_kernel<kOrderWaves, false>), dim3(a.chunks), dim3(64 * kOrderWaves),
+                     kOrderWaves * lds, stream, a);
   return hipGetLastError();
 }
 

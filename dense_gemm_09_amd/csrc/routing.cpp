@@ -108,9 +108,9 @@ gemm_status gemm_route_grad(int64_t T, int64_t E, int64_t top_k, const void* log
 }
 
 size_t gemm_route_order_workspace_size(int64_t S, int64_t G) {
-  if (S <= 0 || S > kMaxDim || G < 0 || G > kMaxOrderGroups) return 0;
+  if (S <= 0 || S > kMaxDim || G < 0 || G > kMaxOrderGroups || order_small(S, G)) return 0;
   int chunk, chunks;
-  order_chunks(S, chunk, chunks);
+  order_chunks(S, G, chunk, chunks);
   return static_cast<size_t>(chunks) * (G + 1) * sizeof(int32_t);
 }
 
@@ -134,7 +134,7 @@ gemm_status gemm_route_order(int64_t S, int64_t G, const int32_t* expert, int32_
   a.counts = static_cast<int32_t*>(workspace);
   a.S = static_cast<int>(S);
   a.G = static_cast<int>(G);
-  order_chunks(S, a.chunk, a.chunks);
+  order_chunks(S, G, a.chunk, a.chunks);
   (void)hipGetLastError();
   return launched(launch_order(a, static_cast<hipStream_t>(stream)));
 }

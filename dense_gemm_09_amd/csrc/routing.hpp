@@ -50,11 +50,17 @@ struct OrderArgs {
   int32_t* order;  // or nullptr
   int32_t* counts; // workspace: [chunks][G + 1]
   int S, G;
-  int chunk, chunks;  // slots per chunk (a multiple of 64)
+  int chunk, chunks;  // slots per chunk (a multiple of 64 per wave)
 };
 
-// The division of S slots into chunks, one wave each.
-void order_chunks(int64_t S, int& chunk, int& chunks);
+// Sorted by one workgroup, which holds the slots' experts in registers and its 16
+// waves' counters in LDS.
+constexpr int kSmallSlots = 8192;
+constexpr int kSmallGroups = 2047;
+inline bool order_small(int64_t S, int64_t G) { return S <= kSmallSlots && G <= kSmallGroups; }
+
+// The division of S slots into chunks.
+void order_chunks(int64_t S, int64_t G, int& chunk, int& chunks);
 hipError_t launch_order(const OrderArgs& a, hipStream_t stream);
 
 struct RowsArgs {
