@@ -1,6 +1,9 @@
 // Routing of tokens to experts, its gradient, and the order of rows by expert.
 // The formulas are in gemm355.h.
 
+#include <algorithm>
+#include <type_traits>
+
 #include "common.hpp"
 #include "routing.hpp"
 
@@ -10,26 +13,84 @@ namespace {
 
 constexpr int kThreads = 256;  // four waves, a token each
 
-__device__ __forceinline__ float load_logit(const void* p, int64_t i, bool bf16) {
-  return bf16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
+typedef unsigned u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef unsigned u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
+  if constexpr (BF16) return bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
+  else return static_cast<const float*>(p)[i];
 }
 
-template <class V>
-__device__ __forceinline__ V wave_sum(V v) {
+// Lane l's experts l * EPL .. l * EPL + EPL - 1 of the row at element `row`; -inf past E.
+template <int EPL, bool BF16>
+__device__ __forceinline__ void load_row(const void* p, int64_t row, int E, int lane, float (&x)[EPL]) {
+  const int e0 = lane * EPL;
+  constexpr int BYTES = EPL * (BF16 ? 2 : 4);
+  if (BYTES >= 8 && e0 + EPL <= E) {
+    const char* at = static_cast<const char*>(p) + (row + e0) * (BF16 ? 2 : 4);
+    uint32_t w[BYTES >= 8 ? BYTES / 4 : 2];
+    if constexpr (BYTES == 8) {
+      const u32x2_any v = *reinterpret_cast<const u32x2_any*>(at);
+      w[0] = v[0];
+      w[1] = v[1];
+    } else if constexpr (BYTES > 8) {
+#pragma unroll
+      for (int h = 0; h < BYTES / 16; ++h) {
+        const u32x4_any v = *reinterpret_cast<const u32x4_any*>(at + 16 * h);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[4 * h + q] = v[q];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      if constexpr (BF16) x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+      else x[i] = __uint_as_float(w[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) x[i] = e0 + i < E ? load_logit<BF16>(p, row + e0 + i) : -__builtin_inff();
+  }
+}
+
+// The value of a wave's last lane after a scan along it that combines neighbours.
+// (Shifts by 1, 2, 4 and 8 lanes within rows of 16, then the rows' last lanes
+// carried over.) Lanes that a shift leaves without a neighbour combine with `idle`.
+template <class F>
+__device__ __forceinline__ int wave_fold(int v, int idle, F combine) {
+  v = combine(v, __builtin_amdgcn_update_dpp(idle, v, 0x111, 0xf, 0xf, false));
+  v = combine(v, __builtin_amdgcn_update_dpp(idle, v, 0x112, 0xf, 0xf, false));
+  v = combine(v, __builtin_amdgcn_update_dpp(idle, v, 0x114, 0xf, 0xf, false));
+  v = combine(v, __builtin_amdgcn_update_dpp(idle, v, 0x118, 0xf, 0xf, false));
+  v = combine(v, __builtin_amdgcn_update_dpp(idle, v, 0x142, 0xa, 0xf, false));
+  v = combine(v, __builtin_amdgcn_update_dpp(idle, v, 0x143, 0xc, 0xf, false));
+  return __builtin_amdgcn_readlane(v, 63);
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+  return __int_as_float(wave_fold(__float_as_int(v), 0, [](int a, int b) {
+    return __float_as_int(__int_as_float(a) + __int_as_float(b));
+  }));
+}
+
+__device__ __forceinline__ int wave_max(int v) {
+  return wave_fold(v, INT32_MIN, [](int a, int b) { return max(a, b); });
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   return v;
 }
 
-template <class V>
-__device__ __forceinline__ V wave_top(V v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const V u = __shfl_xor(v, o);
-    v = u > v ? u : v;
-  }
-  return v;
-}
+// Floats as integers in the same order (-0 below +0: the callers add 0 first),
+// whose maximum needs one instruction. Its own inverse.
+__device__ __forceinline__ int order_key(int bits) { return bits ^ ((bits >> 31) & 0x7fffffff); }
+__device__ __forceinline__ int key_of(float v) { return order_key(__float_as_int(v + 0.f)); }
+__device__ __forceinline__ float value_of(int key) { return __int_as_float(order_key(key)); }
+constexpr int kNoKey = static_cast<int>(0x807fffffu);  // key_of(-inf)
+
+__device__ __forceinline__ float wave_top(float v) { return value_of(wave_max(key_of(v))); }
 
 // The largest value of a wave's lanes and the lowest index that has it.
 __device__ __forceinline__ void wave_best(double& v, int& at) {
@@ -44,71 +105,46 @@ __device__ __forceinline__ void wave_best(double& v, int& at) {
   }
 }
 
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
 // log of the logistic function, without overflow on either side.
 __device__ __forceinline__ float log_sigmoid(float x) { return fminf(x, 0.f) - log1pf(expf(-fabsf(x))); }
 
 }  // namespace
 
 // ------------------------------------------------------------------ choice
+//
+// One wave per token; a lane has EPL neighbouring experts. Everything a choice
+// needs of the whole row is a wave's scan (six instructions) and scalar from
+// there on: the best key is found with a maximum, its expert from the lanes' equality
+// masks, lowest lane and lowest element first, in scalar registers. With E = 256
+// a round is 17 vector instructions.
+//
+// Without a bias the keys are the logits. With one, scores are first formed in
+// FP32, each within `slack` of its exact value; where two neighbours in the order
+// found (or the last group kept and the first not) are closer than that decides,
+// the token is done again with scores in 64 bits. With 256 experts, random logits
+// and a bias that happens to one token in 700; 64-bit scores for all of them took
+// 98 us for 16384 tokens, this 49.
 
-// One wave per token; lane l holds experts l, l + 64, ... (EPL of them).
+// One token's choice with scores in 64 bits. id: lane j's expert (-1: none left).
 template <int EPL>
-__global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p, bool bf16) {
-  const int lane = threadIdx.x & 63;
-  const float ninf = -__builtin_inff();
-  for (int t = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); t < p.T; t += gridDim.x * (kThreads / 64)) {
-
-  float x[EPL];
-  bool bad = false;
-  float top = ninf;
+__device__ __forceinline__ void choose_exactly(const RouteArgs& p, const float (&x)[EPL], const float (&bias)[EPL],
+                                               float base, int lane, int& id) {
+  const double ninf = -__builtin_inf();
+  double c[EPL], all = 1.0;
+  if (!p.sigmoid) {
+    all = 0.0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) all += exp(static_cast<double>(x[i]) - base);
+    all = wave_sum(all);
+  }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 64 * i;
-    x[i] = e < p.E ? load_logit(p.logits, t * p.ldl + e, bf16) : ninf;
-    bad = bad || x[i] != x[i] || (!p.sigmoid && x[i] == -ninf);
-    top = fmaxf(top, x[i]);
+    const double xd = x[i];
+    const double v = (p.sigmoid ? 1.0 / (1.0 + exp(-xd)) : exp(xd - base) / all) + bias[i];
+    c[i] = x[i] > -__builtin_inff() && v == v ? v : ninf;
   }
-  int32_t* expert = p.expert + static_cast<int64_t>(t) * p.top_k;
-  float* weight = p.weight + static_cast<int64_t>(t) * p.top_k;
-  if (__any(bad)) {
-    if (lane < p.top_k) {
-      expert[lane] = -1;
-      weight[lane] = __builtin_nanf("");
-    }
-    continue;
-  }
-  top = wave_top(top);
-  const float base = p.sigmoid || top == ninf ? 0.f : top;
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) sum += expf(x[i] - base);
-  sum = wave_sum(sum);
-
-  // Scores to choose by, in 64 bits: experts whose scores differ in their last
-  // bits are told apart. Without a bias they are the logits.
-  const bool by_logit = p.bias == nullptr && p.group_best == 1;
-  double c[EPL];
-  if (by_logit) {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) c[i] = x[i];
-  } else {
-    double all = 1.0;
-    if (!p.sigmoid) {
-      all = 0.0;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) all += exp(static_cast<double>(x[i]) - base);
-      all = wave_sum(all);
-    }
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + 64 * i;
-      const double xd = x[i];
-      double v = p.sigmoid ? 1.0 / (1.0 + exp(-xd)) : exp(xd - base) / all;
-      if (p.bias != nullptr && e < p.E) v += p.bias[e];
-      c[i] = x[i] > ninf && v == v ? v : ninf;
-    }
-  }
-
   if (p.groups > 1) {
     const int per = p.E / p.groups;
     double mine = ninf;  // score of group `lane`
@@ -120,8 +156,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p, bool bf16)
         int at = 1 << 30;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-          const int e = lane + 64 * i;
-          if (e / per == g && e < p.E && e != first && c[i] > v) {
+          const int e = lane * EPL + i;
+          if (e >= g * per && e < (g + 1) * per && e != first && c[i] > v) {
             v = c[i];
             at = e;
           }
@@ -140,154 +176,379 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p, bool bf16)
     const unsigned long long keep = __ballot(lane < p.groups && rank < p.top_groups);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int e = lane + 64 * i;
+      const int e = lane * EPL + i;
       if (e < p.E && !((keep >> (e / per)) & 1)) c[i] = ninf;
     }
   }
-
-  int id = -1;  // lane j: the j-th expert and its logit
-  float xj = ninf;
+  id = -1;
   for (int j = 0; j < p.top_k; ++j) {
     double v = ninf;
     int at = 1 << 30;
-    float xv = ninf;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       if (c[i] > v) {
         v = c[i];
-        at = lane + 64 * i;
-        xv = x[i];
+        at = lane * EPL + i;
       }
     }
     wave_best(v, at);
     if (!(v > ninf)) break;
-    xv = __shfl(xv, at & 63);
-    if (lane == j) {
-      id = at;
-      xj = xv;
-    }
+    if (lane == j) id = at;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (lane + 64 * i == at) c[i] = ninf;
+      if (lane * EPL + i == at) c[i] = ninf;
   }
+}
 
-  float w = 0.f;
-  if (p.renormalise) {
-    const float ls = p.sigmoid ? log_sigmoid(xj) : xj;
-    const float most = wave_top(id >= 0 ? ls : ninf);
-    const float s = id >= 0 ? expf(ls - most) : 0.f;
-    const float z = wave_sum(s);
-    w = id >= 0 ? p.scale * (s / z) : 0.f;
-  } else if (id >= 0) {
-    w = p.scale * (p.sigmoid ? expf(log_sigmoid(xj)) : expf(xj - base) / sum);
+// The lane `step` away within 16 lanes, for butterflies: pairs, quads, and then
+// mirrored halves, whose lanes agree by then.
+template <int STEP>
+__device__ __forceinline__ int across(int v) {
+  constexpr int CTRL = STEP == 1 ? 0xb1 : STEP == 2 ? 0x4e : STEP == 4 ? 0x141 : 0x140;
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, true);
+}
+
+// The scores of the groups, group g's in lane g: the sum of its one or two best
+// keys. In the usual case a group is 2, 4, 8 or 16 lanes whole, which find its two
+// best in a butterfly, all groups at once; otherwise it is one group after another
+// (256 experts in 8 groups, 16384 tokens: 49 us, one after another 57).
+template <int EPL>
+__device__ __forceinline__ float group_scores(const RouteArgs& p, const int (&key)[EPL], int lane) {
+  const int per = p.E / p.groups, lanes = per / EPL;
+  float mine = -__builtin_inff();
+  if (lanes * EPL == per && (lanes & (lanes - 1)) == 0 && lanes >= 1 && lanes <= 16) {
+    int a = kNoKey, b = kNoKey;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      b = max(b, min(a, key[i]));
+      a = max(a, key[i]);
+    }
+    const auto join = [&](int a2, int b2) {
+      b = max(max(b, b2), min(a, a2));
+      a = max(a, a2);
+    };
+    if (lanes > 1) join(across<1>(a), across<1>(b));
+    if (lanes > 2) join(across<2>(a), across<2>(b));
+    if (lanes > 4) join(across<4>(a), across<4>(b));
+    if (lanes > 8) join(across<8>(a), across<8>(b));
+    float total = value_of(a);
+    if (p.group_best == 2 && b != kNoKey) total += value_of(b);
+    const float there = __shfl(total, (lane * lanes) & 63);
+    return lane < p.groups ? there : mine;
   }
-  if (lane < p.top_k) {
-    expert[lane] = id;
-    weight[lane] = w;
+  for (int g = 0; g < p.groups; ++g) {
+    int a = kNoKey, b = kNoKey;
+    const int lo = g * per - lane * EPL, hi = lo + per;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int k = i >= lo && i < hi ? key[i] : kNoKey;
+      b = max(b, min(a, k));
+      a = max(a, k);
+    }
+    const int best = wave_max(a);
+    float total = value_of(best);
+    if (p.group_best == 2 && best != kNoKey) {
+      const int owner = __builtin_ctzll(__ballot(a == best));
+      const int second = wave_max(lane == owner ? b : a);
+      if (second != kNoKey) total += value_of(second);
+    }
+    if (lane == g) mine = total;
   }
+  return mine;
+}
+
+// Removes the experts outside the best groups from `key`. Returns whether
+// slack leaves the groups in doubt.
+template <int EPL>
+__device__ __forceinline__ bool keep_groups(const RouteArgs& p, int (&key)[EPL], int lane, float slack) {
+  const int per = p.E / p.groups;
+  const float mine = group_scores<EPL>(p, key, lane);
+  int rank = 0;
+  for (int g = 0; g < p.groups; ++g) {
+    const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), g));
+    rank += (v > mine) | ((v == mine) & (g < lane)) ? 1 : 0;
+  }
+  const bool kept = lane < p.groups && rank < p.top_groups;
+  const unsigned long long keep = __ballot(kept);
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane * EPL + i;
+    key[i] = (keep >> ((e / per) & 63)) & 1 ? key[i] : kNoKey;  // (past E there is none anyway)
+  }
+  if (p.top_groups == p.groups) return false;
+  const float last = -wave_top(kept ? -mine : -__builtin_inff());
+  const float next = wave_top(kept ? -__builtin_inff() : mine);
+  // (Groups without an expert left are -inf on both sides: inf - inf is NaN, no doubt.)
+  return last - next <= 4.f * slack;
+}
+
+// SCORED: keys are scores (a bias, or groups by two scores), not logits.
+template <int EPL, bool BF16, bool SCORED>
+__global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const float ninf = -__builtin_inff();
+  const float most_allowed = p.sigmoid ? __builtin_inff() : __FLT_MAX__;
+  const int step = gridDim.x * (kThreads / 64);
+  int t = blockIdx.x * (kThreads / 64) + wave;
+  if (t >= p.T) return;
+
+  float bias[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) bias[i] = 0.f;
+  if constexpr (SCORED) {
+    if (p.bias != nullptr) load_row<EPL, false>(p.bias, 0, p.E, lane, bias);  // (past E -inf: no key)
+  }
+  float x[EPL];
+  load_row<EPL, BF16>(p.logits, t * p.ldl, p.E, lane, x);
+  for (;;) {
+    int32_t* expert = p.expert + static_cast<int64_t>(t) * p.top_k;
+    float* weight = p.weight + static_cast<int64_t>(t) * p.top_k;
+    // The next token's logits are on their way while this one's are sorted out.
+    t += step;
+    const bool more = t < p.T;
+    float next[EPL];
+    if (more) load_row<EPL, BF16>(p.logits, t * p.ldl, p.E, lane, next);
+
+    float top = ninf;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      bad |= !(x[i] <= most_allowed);
+      top = x[i] > top ? x[i] : top;
+    }
+    int id = -1;
+    float w = 0.f;
+    if (__any(bad)) {
+      w = __builtin_nanf("");
+    } else {
+      // Softmax: the row's largest logit and the sum. Both scores and weights as
+      // they are need it, shares of the chosen do not.
+      float base = 0.f, sum = 1.f;
+      if (!p.sigmoid && (SCORED || !p.renormalise)) {
+        top = wave_top(top);
+        base = top == ninf ? 0.f : top;
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) sum += fast_exp(x[i] - base);
+        sum = wave_sum(sum);
+      }
+
+      int key[EPL];
+      float slack = 0.f;
+      if constexpr (!SCORED) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) key[i] = key_of(x[i]);
+      } else {
+        // How far a c may be off: the exponential of an argument off by 2^-24 of itself and
+        // one more step of 2^-23, the reciprocal's, and half a step of the sum with
+        // the bias. A sigmoid, at most 1, comes to 2^-22; a softmax's, at most 1 / sum,
+        // to 2^-22 of that and the 22 roundings of the sum.
+        float most = 0.f;
+        const float inverse = 1.f / sum;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          const float s = p.sigmoid ? __builtin_amdgcn_rcpf(1.f + fast_exp(-x[i])) : fast_exp(x[i] - base) * inverse;
+          const float c = s + bias[i];
+          const bool there = (x[i] > ninf) & (c > ninf);  // (false for a NaN)
+          key[i] = there ? key_of(c) : kNoKey;
+          most = there & (fabsf(c) > most) ? fabsf(c) : most;
+        }
+        slack = (p.sigmoid ? 0x1p-20f : 0x1p-19f * inverse) + 0x1p-22f * wave_top(most);
+      }
+      bool doubt = false;
+      if (p.groups > 1) doubt = keep_groups<EPL>(p, key, lane, slack);
+
+      // Rounds: slot j's expert goes to lane j. One round more tells how near the
+      // first expert left out is.
+      float before = __builtin_inff();
+      const int rounds = SCORED ? p.top_k + 1 : p.top_k;
+      for (int j = 0; j < rounds; ++j) {
+        int v = key[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) v = max(v, key[i]);
+        const int best = wave_max(v);
+        if (best == kNoKey) break;
+        const int owner = __builtin_ctzll(__ballot(v == best));
+        // The lowest element of the owner's that has it.
+        int at = EPL - 1;
+#pragma unroll
+        for (int i = EPL - 2; i >= 0; --i)
+          if ((__ballot(key[i] == best) >> owner) & 1) at = i;
+        if constexpr (SCORED) {
+          const float here = value_of(best);
+          doubt |= before - here <= 2.f * slack;
+          before = here;
+        }
+        id = lane == j ? owner * EPL + at : id;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) key[i] = (lane == owner) & (i == at) ? kNoKey : key[i];
+      }
+      if (lane >= p.top_k) id = -1;
+      if constexpr (SCORED) {
+        if (__any(doubt)) choose_exactly<EPL>(p, x, bias, base, lane, id);
+      }
+
+      float xj = ninf;  // its logit, from the lane that has it
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const float u = __shfl(x[i], (id >= 0 ? id : 0) / EPL);
+        xj = (id >= 0) & (id % EPL == i) ? u : xj;
+      }
+      if (p.renormalise) {
+        const float ls = p.sigmoid ? log_sigmoid(xj) : xj;
+        const float most = wave_top(id >= 0 ? ls : ninf);
+        const float s = id >= 0 ? expf(ls - most) : 0.f;
+        const float z = wave_sum(s);
+        w = id >= 0 ? p.scale * (s / z) : 0.f;
+      } else if (id >= 0) {
+        w = p.scale * (p.sigmoid ? expf(log_sigmoid(xj)) : expf(xj - base) / sum);
+      }
+    }
+    if (lane < p.top_k) {
+      expert[lane] = id;
+      weight[lane] = w;
+    }
+    if (!more) return;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) x[i] = next[i];
   }
 }
 
 // ---------------------------------------------------------------- gradient
 
-// One wave per token; lane j has slot j while the slots' gradients are formed.
-template <int EPL>
-__global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs p, bool bf16) {
+// One wave per token; lane j has slot j while the slots' gradients are formed,
+// then lanes have neighbouring experts as above. The whole row is written, zeros
+// mostly, which bounds it.
+template <int EPL, bool BF16>
+__global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs p) {
   const int lane = threadIdx.x & 63;
-  for (int t = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); t < p.T; t += gridDim.x * (kThreads / 64)) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float ninf = -__builtin_inff();
   const bool full = !p.sigmoid && !p.renormalise;  // every logit has a gradient
-
-  int id = -1;
-  float dw = 0.f, xj = ninf;
-  if (lane < p.top_k) {
-    id = p.expert[static_cast<int64_t>(t) * p.top_k + lane];
-    if (id < 0 || id >= p.E) id = -1;
-    if (id >= 0) {
-      dw = p.scale * p.dweight[static_cast<int64_t>(t) * p.top_k + lane];
-      xj = load_logit(p.logits, t * p.ldl + id, bf16);
+  for (int t = blockIdx.x * (kThreads / 64) + wave; t < p.T; t += gridDim.x * (kThreads / 64)) {
+    const int64_t row = t * p.ldl;
+    int id = -1;
+    float dw = 0.f, xj = ninf;
+    if (lane < p.top_k) {
+      id = p.expert[static_cast<int64_t>(t) * p.top_k + lane];
+      if (id < 0 || id >= p.E) id = -1;
+      if (id >= 0) {
+        dw = p.scale * p.dweight[static_cast<int64_t>(t) * p.top_k + lane];
+        xj = load_logit<BF16>(p.logits, row + id);
+      }
     }
-  }
+    const bool none = !__any(id >= 0);
 
-  float x[EPL], base = 0.f, sum = 1.f;
-  if (full) {
-    float top = ninf;
+    float x[EPL], base = 0.f, sum = 1.f;
+    if (full) {
+      load_row<EPL, BF16>(p.logits, row, p.E, lane, x);
+      float top = ninf;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + 64 * i;
-      x[i] = e < p.E ? load_logit(p.logits, t * p.ldl + e, bf16) : ninf;
-      top = fmaxf(top, x[i]);
+      for (int i = 0; i < EPL; ++i) top = x[i] > top ? x[i] : top;
+      top = wave_top(top);
+      base = top == ninf ? 0.f : top;
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        x[i] = fast_exp(x[i] - base);
+        sum += x[i];
+      }
+      sum = wave_sum(sum);
     }
-    top = wave_top(top);
-    base = top == ninf ? 0.f : top;
-    sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) sum += expf(x[i] - base);
-    sum = wave_sum(sum);
-  }
 
-  float v = 0.f, dot = 0.f;
-  if (p.renormalise) {
-    const float ls = p.sigmoid ? log_sigmoid(xj) : xj;
-    const float most = wave_top(id >= 0 ? ls : ninf);
-    const float s = id >= 0 && most > ninf ? expf(ls - most) : 0.f;
-    const float z = wave_sum(s);
-    const float share = s > 0.f ? s / z : 0.f;
-    const float mean = wave_sum(id >= 0 ? dw * share : 0.f);
-    v = id >= 0 ? share * (dw - mean) : 0.f;
-    if (p.sigmoid && id >= 0) v *= 1.f / (1.f + expf(xj));
-  } else if (p.sigmoid) {
-    // s (1 - s), both factors to their relative accuracy
-    if (id >= 0) v = dw * expf(log_sigmoid(xj)) * (1.f / (1.f + expf(xj)));
-  } else {
-    v = id >= 0 ? dw * (expf(xj - base) / sum) : 0.f;
-    dot = wave_sum(v);
-  }
-  const bool none = !__any(id >= 0);
+    float v = 0.f, dot = 0.f;
+    if (p.renormalise) {
+      const float ls = p.sigmoid ? log_sigmoid(xj) : xj;
+      const float most = wave_top(id >= 0 ? ls : ninf);
+      const float s = id >= 0 && most > ninf ? expf(ls - most) : 0.f;
+      const float z = wave_sum(s);
+      const float share = s > 0.f ? s / z : 0.f;
+      const float mean = wave_sum(id >= 0 ? dw * share : 0.f);
+      v = id >= 0 ? share * (dw - mean) : 0.f;
+      if (p.sigmoid && id >= 0) v *= 1.f / (1.f + expf(xj));
+    } else if (p.sigmoid) {
+      // s (1 - s), both factors to their relative accuracy
+      if (id >= 0) v = dw * expf(log_sigmoid(xj)) * (1.f / (1.f + expf(xj)));
+    } else {
+      v = id >= 0 ? dw * (expf(xj - base) / sum) : 0.f;
+      dot = wave_sum(v);
+    }
 
-  float d[EPL];
+    float d[EPL];
+    const float f = full && !none ? -dot / sum : 0.f;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) d[i] = full && !none ? -dot * (expf(x[i] - base) / sum) : 0.f;
-  for (int j = 0; j < p.top_k; ++j) {
-    const int at = __shfl(id, j);
-    const float add = __shfl(v, j);
+    for (int i = 0; i < EPL; ++i) d[i] = full && !none ? f * x[i] : 0.f;
+    const int e0 = lane * EPL;
+    for (int j = 0; j < p.top_k; ++j) {
+      const int at = __builtin_amdgcn_readlane(id, j) - e0;
+      const float add = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j));
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (lane + 64 * i == at) d[i] += add;
-  }
+      for (int i = 0; i < EPL; ++i) d[i] += i == at ? add : 0.f;
+    }
+
+    const int64_t out = t * p.ldd + e0;
+    constexpr int WORDS = BF16 ? EPL / 2 : EPL;
+    if (WORDS >= 2 && e0 + EPL <= p.E) {
+      uint32_t w[WORDS >= 2 ? WORDS : 2];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 64 * i;
-    if (e >= p.E) continue;
-    if (bf16) static_cast<uint16_t*>(p.dlogits)[t * p.ldd + e] = f32_to_bf16_bits(d[i]);
-    else static_cast<float*>(p.dlogits)[t * p.ldd + e] = d[i];
-  }
+      for (int i = 0; i < WORDS; ++i) {
+        if constexpr (BF16) w[i] = f32x2_to_bf16x2_bits(d[2 * i], d[2 * i + 1]);
+        else w[i] = __float_as_uint(d[i]);
+      }
+      char* at = static_cast<char*>(p.dlogits) + out * (BF16 ? 2 : 4);
+      if constexpr (WORDS == 2) *reinterpret_cast<u32x2_any*>(at) = u32x2_any{w[0], w[1]};
+#pragma unroll
+      for (int h = 0; h < WORDS / 4; ++h)
+        *reinterpret_cast<u32x4_any*>(at + 16 * h) = u32x4_any{w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        if (e0 + i >= p.E) continue;
+        if constexpr (BF16) static_cast<uint16_t*>(p.dlogits)[out + i] = f32_to_bf16_bits(d[i]);
+        else static_cast<float*>(p.dlogits)[out + i] = d[i];
+      }
+    }
   }
 }
 
-template <class Args, class F>
-static hipError_t launch_rows_of_experts(const Args& a, bool bf16, F kernel_of, hipStream_t stream) {
-  const int wgs = (a.T + kThreads / 64 - 1) / (kThreads / 64);
-  const dim3 grid(static_cast<unsigned>(wgs < kMaxGrid ? wgs : kMaxGrid)), block(kThreads);
-  const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, bf16); };
-  kernel_of(go);
-  return hipGetLastError();
+// Workgroups of gemm_route at most: those that are on the card at once.
+constexpr int kRouteGrid = 256 * 5;
+
+// Experts per lane for E of them.
+template <class Go>
+static void with_experts_per_lane(int E, Go go) {
+  if (E <= 64) go(std::integral_constant<int, 1>{});
+  else if (E <= 128) go(std::integral_constant<int, 2>{});
+  else if (E <= 256) go(std::integral_constant<int, 4>{});
+  else if (E <= 512) go(std::integral_constant<int, 8>{});
+  else go(std::integral_constant<int, 16>{});
+}
+
+static dim3 token_grid(int T) {
+  const int wgs = (T + kThreads / 64 - 1) / (kThreads / 64);
+  return dim3(static_cast<unsigned>(wgs < kMaxGrid ? wgs : kMaxGrid));
 }
 
 hipError_t launch_route(const RouteArgs& a, bool bf16, hipStream_t stream) {
-  return launch_rows_of_experts(a, bf16, [&](auto go) {
-    if (a.E <= 64) go(route_kernel<1>);
-    else if (a.E <= 256) go(route_kernel<4>);
-    else go(route_kernel<16>);
-  }, stream);
+  const dim3 grid(static_cast<unsigned>(std::min((a.T + kThreads / 64 - 1) / (kThreads / 64), kRouteGrid)));
+  const auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a); };
+  const bool scored = a.bias != nullptr || (a.groups > 1 && a.group_best == 2);
+  with_experts_per_lane(a.E, [&](auto n) {
+    constexpr int EPL = decltype(n)::value;
+    if (scored) bf16 ? run(route_kernel<EPL, true, true>) : run(route_kernel<EPL, false, true>);
+    else bf16 ? run(route_kernel<EPL, true, false>) : run(route_kernel<EPL, false, false>);
+  });
+  return hipGetLastError();
 }
 
 hipError_t launch_route_grad(const RouteGradArgs& a, bool bf16, hipStream_t stream) {
-  return launch_rows_of_experts(a, bf16, [&](auto go) {
-    if (a.E <= 64) go(route_grad_kernel<1>);
-    else if (a.E <= 256) go(route_grad_kernel<4>);
-    else go(route_grad_kernel<16>);
-  }, stream);
+  const auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, token_grid(a.T), dim3(kThreads), 0, stream, a); };
+  with_experts_per_lane(a.E, [&](auto n) {
+    constexpr int EPL = decltype(n)::value;
+    bf16 ? run(route_grad_kernel<EPL, true>) : run(route_grad_kernel<EPL, false>);
+  });
+  return hipGetLastError();
 }
 
 // ------------------------------------------------------------- order of rows
