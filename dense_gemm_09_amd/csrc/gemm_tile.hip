@@ -672,12 +672,19 @@ __device__ __forceinline__ void run_epilogue(const GemmArgs& p,
 // every adapter in it: neighbours mostly share one. Every adapter's product has
 // an accumulator of its own, from which the rows that have that adapter are
 // taken, so that an adapter's infinities and NaN reach no other row.
-// Fragments come straight from memory: h is small and stays in cache, and a
-// tile's columns of an adapter are read by the waves of one tile row.
+// Fragments come straight from memory (h is small and stays in cache, and a
+// tile's columns of an adapter are read by the waves of one tile row), 32 ranks of
+// them requested together: it is their latency that this costs. Where K is split,
+// an adapter goes to the partial sum of its number (not of its turn in the batch:
+// a row's bits do not depend on its neighbours).
 template <class C>
 __device__ __forceinline__ void add_adapters(const LoraArgs& p, f32x16 (&acc)[C::FM][C::FN], int row0,
-                                             int col0, int lane) {
+                                             int col0, int lane, int split) {
+  constexpr int TU = 2;  // 16 ranks each
   const int half = lane >> 5, l = lane & 31;
+  const uint16_t* up[C::FN];
+#pragma unroll
+  for (int j = 0; j < C::FN; ++j) up[j] = p.up + min(col0 + 32 * j + l, p.N - 1) * p.ld_up;
 #pragma unroll
   for (int i = 0; i < C::FM; ++i) {
     const int m = row0 + 32 * i + l;
@@ -692,32 +699,39 @@ __device__ __forceinline__ void add_adapters(const LoraArgs& p, f32x16 (&acc)[C:
     do {
       const int g = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
       left &= ~static_cast<unsigned>(__ballot(id == g));
+      if (g % p.split_k != split) continue;
+      const int64_t at = g * p.stride_up;
+      f32x16 d[C::FN];
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j) {
-        const int n = min(col0 + 32 * j + l, p.N - 1);
-        const uint16_t* u = p.up + g * p.stride_up + n * p.ld_up;
-        f32x16 d;
+      for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) d[e] = 0.f;
-        for (int t = 0; t < p.pad; t += 16) {
-          // Columns past the rank are zeros in h, and have to be here too: what
-          // lies there belongs to another row.
-          const int r = t + 8 * half;
-          i32x4 b = {0, 0, 0, 0};
-          if (p.up_vec) {
-            if (r < p.rank) b = *reinterpret_cast<const i32x4*>(u + r);
-          } else {
+        for (int e = 0; e < 16; ++e) d[j][e] = 0.f;
+      for (int t0 = 0; t0 < p.pad; t0 += 16 * TU) {
+        i32x4 high[TU], low[TU], u[TU][C::FN];
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              if (r + q < p.rank) b[q >> 1] |= static_cast<int>(static_cast<uint32_t>(u[r + q]) << (16 * (q & 1)));
+        for (int t = 0; t < TU; ++t) {
+          const int r = t0 + 16 * t;
+          high[t] = low[t] = i32x4{0, 0, 0, 0};
+          if (r < p.pad) {
+            high[t] = *reinterpret_cast<const i32x4*>(h + r);
+            low[t] = *reinterpret_cast<const i32x4*>(h + p.pad + r);
           }
-          const bf16x8 bu = __builtin_bit_cast(bf16x8, b);
-          d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(h + t), bu, d, 0, 0, 0);
-          d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(h + p.pad + t), bu, d, 0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < C::FN; ++j) u[t][j] = load8(up[j] + at, r + 8 * half, p.rank);
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][j][e] += own[e] == g ? d[e] : 0.f;
+        for (int t = 0; t < TU; ++t)
+#pragma unroll
+          for (int j = 0; j < C::FN; ++j) {
+            const bf16x8 b = __builtin_bit_cast(bf16x8, u[t][j]);
+            d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, high[t]), b, d[j], 0, 0, 0);
+            d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, low[t]), b, d[j], 0, 0, 0);
+          }
       }
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] += own[e] == g ? d[j][e] : 0.f;
     } while (left != 0);
   }
 }
@@ -1308,7 +1322,7 @@ gemm_tile_kernel(ArgsOf<MODE> p) {
   const int row0 = m0 + wm0, col0 = n0 + wn0;
   if constexpr (MODE == MODE_LORA) {
     // (Without adapters there are no arrays of them to read.)
-    if (p.adapters > 0 && (!SPLIT || split == 0)) add_adapters<C>(p, acc, row0, col0, lane);
+    if (p.adapters > 0) add_adapters<C>(p, acc, row0, col0, lane, split);
   }
   run_epilogue<C, OUT, SPLIT>(p, acc, elds, row0, col0, lane, split);
 }

@@ -108,7 +108,6 @@ gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R
   a.adapters = adapters ? static_cast<int>(G) : 0;
   a.rank = static_cast<int>(R);
   a.pad = static_cast<int>(padded_rank(R));
-  a.up_vec = R % 8 == 0 && ld_up % 8 == 0 && stride_up % 8 == 0 && aligned(up, 16) ? 1 : 0;
   (void)hipGetLastError();  // an earlier call's pending error is not this call's
   if (adapters) {
     LoraDownArgs d{};

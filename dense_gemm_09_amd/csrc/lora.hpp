@@ -24,8 +24,23 @@ struct LoraArgs : GemmArgs {
   int64_t ld_up, stride_up;
   int adapters;            // G
   int rank, pad;
-  int up_vec;              // 1: rows of up are 16-byte aligned and hold pad elements
 };
+
+typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+// Elements k .. k+7 of a BF16 row of K at any alignment; zeros past its end (what lies
+// there belongs to another row).
+__device__ __forceinline__ i32x4 load8(const uint16_t* row, int k, int K) {
+  i32x4 v = {0, 0, 0, 0};
+  if (k + 8 <= K) {
+    v = *reinterpret_cast<const i32x4_any*>(row + k);
+  } else if (k < K) {
+#pragma unroll
+    for (int q = 0; q < 7; ++q)
+      if (k + q < K) v[q >> 1] |= static_cast<int>(static_cast<uint32_t>(row[k + q]) << (16 * (q & 1)));
+  }
+  return v;
+}
 
 struct LoraDownArgs {
   const uint16_t* A;
