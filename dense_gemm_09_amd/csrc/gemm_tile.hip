@@ -692,14 +692,13 @@ __device__ __forceinline__ void add_adapters(const LoraArgs& p, f32x16 (&acc)[C:
     id = id < p.adapters ? id : -1;
     unsigned left = static_cast<unsigned>(__ballot(id >= 0));  // lanes 32.. repeat these rows
     if (left == 0) continue;
-    int own[16];  // adapters of the accumulators' rows
-#pragma unroll
-    for (int e = 0; e < 16; ++e) own[e] = __shfl(id, 8 * (e >> 2) + 4 * half + (e & 3));
     const uint16_t* h = p.h + static_cast<int64_t>(min(m, p.M - 1)) * (2 * p.pad) + 8 * half;
     do {
       const int g = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-      left &= ~static_cast<unsigned>(__ballot(id == g));
+      const unsigned rows = static_cast<unsigned>(__ballot(id == g));
+      left &= ~rows;
       if (g % p.split_k != split) continue;
+      const unsigned own = rows >> (4 * half);  // bit 8 (e / 4) + e % 4: the row of accumulator e
       const int64_t at = g * p.stride_up;
       f32x16 d[C::FN];
 #pragma unroll
@@ -731,7 +730,7 @@ __device__ __forceinline__ void add_adapters(const LoraArgs& p, f32x16 (&acc)[C:
 #pragma unroll
       for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][j][e] += own[e] == g ? d[j][e] : 0.f;
+        for (int e = 0; e < 16; ++e) acc[i][j][e] += (own >> (8 * (e >> 2) + (e & 3))) & 1 ? d[j][e] : 0.f;
     } while (left != 0);
   }
 }
@@ -741,11 +740,19 @@ __device__ __forceinline__ void add_adapters(const LoraArgs& p, f32x16 (&acc)[C:
 template <int MODE>
 using ArgsOf = std::conditional_t<MODE == MODE_LORA, LoraArgs, GemmArgs>;
 
+// What the adapters need after the main loop must not cost the 128x128 tile the
+// second workgroup on a CU.
+#if defined(G355_LORA)
+#define G355_WAVES_PER_SIMD __attribute__((amdgpu_waves_per_eu(C::BM == 128 ? 2 : 1)))
+#else
+#define G355_WAVES_PER_SIMD
+#endif
+
 // RAGGED: K may end inside a 16-byte chunk of a DMA-fed row (patch_tail).
 // Kept out of the other instantiations: the patch's code perturbs the
 // register allocation of the K loop.
 template <class C, int LA, int LB, int OUT, bool SPLIT, bool RAGGED, int MODE = MODE_DENSE>
-__global__ void __launch_bounds__(C::NT)
+__global__ void __launch_bounds__(C::NT) G355_WAVES_PER_SIMD
 gemm_tile_kernel(ArgsOf<MODE> p) {
   // The LDS block holds the ring of K slices, and after the main loop the
   // epilogue's staging strips.

@@ -23,9 +23,12 @@ constexpr int64_t k2G = int64_t{1} << 31;
 bool bad_dim(int64_t v) { return v < 0 || v > kMaxDim; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// Bytes of h, in front of the partial sums of a split K.
-size_t h_bytes(int64_t M, int64_t R) {
-  return (static_cast<size_t>(M) * 4 * padded_rank(R) + 255) / 256 * 256;
+// The workspace: h, its partial sums, the product's partial sums of a split K.
+size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
+size_t h_bytes(int64_t M, int64_t R) { return rounded(static_cast<size_t>(M) * 4 * padded_rank(R)); }
+size_t partial_bytes(int64_t M, int64_t K, int64_t R) {
+  const int shares = lora_shares(M, K, R).shares;
+  return shares == 1 ? 0 : rounded(static_cast<size_t>(shares) * M * padded_rank(R) * sizeof(float));
 }
 
 }  // namespace
@@ -42,7 +45,7 @@ extern "C" {
 
 size_t gemm_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t R) {
   if (M <= 0 || N <= 0 || bad_dim(M) || bad_dim(N) || bad_dim(K) || R < 0 || R > kMaxRank) return 0;
-  return h_bytes(M, R) + make_tile_plan(M, N, K, false).workspace;
+  return h_bytes(M, R) + partial_bytes(M, K, R) + make_tile_plan(M, N, K, false).workspace;
 }
 
 gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R, float alpha,
@@ -84,7 +87,7 @@ gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R
   a.B = B;
   a.C = C;
   a.bias = static_cast<const uint16_t*>(bias);
-  a.workspace = reinterpret_cast<float*>(static_cast<char*>(workspace) + h_bytes(M, R));
+  a.workspace = reinterpret_cast<float*>(static_cast<char*>(workspace) + h_bytes(M, R) + partial_bytes(M, K, R));
   a.lda = lda;
   a.ldb = ldb;
   a.ldc = ldc;
@@ -101,7 +104,7 @@ gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R
   a.tiles_m = static_cast<int>((M + plan.bm - 1) / plan.bm);
   a.tiles_n = static_cast<int>((N + plan.bn - 1) / plan.bn);
   a.adapter = adapter;
-  a.h = static_cast<uint16_t*>(workspace);
+  a.h = static_cast<const uint16_t*>(workspace);
   a.up = static_cast<const uint16_t*>(up);
   a.ld_up = ld_up;
   a.stride_up = stride_up;
@@ -118,7 +121,11 @@ gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R
     d.ld_down = ld_down;
     d.stride_down = stride_down;
     d.scale = scale;
-    d.h = a.h;
+    const LoraShares shares = lora_shares(M, K, R);
+    d.h = static_cast<uint16_t*>(workspace);
+    d.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + h_bytes(M, R));
+    d.shares = shares.shares;
+    d.share_len = shares.len;
     d.M = a.M;
     d.K = a.K;
     d.adapters = a.adapters;

@@ -2,6 +2,8 @@
 // next to the product's, and the launch of the first factor's product.
 #pragma once
 
+#include <algorithm>
+
 #include "common.hpp"
 
 namespace g355 {
@@ -12,14 +14,31 @@ constexpr int64_t kMaxAdapters = int64_t{1} << 16;
 // Rank as the matrix cores take it: a multiple of an MFMA's 16 K elements.
 inline int64_t padded_rank(int64_t R) { return (R + 15) / 16 * 16; }
 
-// H holds, for row m with adapter a, h = scale[a] * (A[m] down_a) as two BF16
-// values: pad high parts RNE(h), then pad low parts RNE(h - high). h is off by
-// at most 2^-16 of itself, where one BF16 value would be off by 2^-8: as much as
-// the output's own rounding, before it. Columns from the rank on are zeros, and so
-// are rows without an adapter.
+// The first factors' product h[m] = scale[a] * (A[m] down_a) of row m with adapter a.
+// It is summed in FP32, over shares of K where that brings more workgroups, and
+// handed to the second factors as two BF16 values: pad high parts RNE(h), then
+// pad low parts RNE(h - high). Off by at most 2^-16 of h, where one BF16 value would be
+// off by 2^-8: as much as the output's own rounding, before it. Columns from the
+// rank on are zeros; rows without an adapter are not written.
+struct LoraShares {
+  int shares;
+  int len;  // K elements of a share, a multiple of 64
+};
+
+// Workgroups that the first factors' product is spread over: one on every CU.
+constexpr int64_t kLoraWorkgroups = 256;
+
+inline LoraShares lora_shares(int64_t M, int64_t K, int64_t R) {
+  const int64_t units = (M + 15) / 16 * std::max<int64_t>(1, padded_rank(R) / 16);
+  const int64_t most = M > 64 ? 1 : std::min<int64_t>(4, std::max<int64_t>(1, kLoraWorkgroups / units));
+  const int64_t shares = std::max<int64_t>(1, std::min(most, (K + 1023) / 1024));
+  const int64_t len = std::max<int64_t>(64, ((K + shares - 1) / shares + 63) / 64 * 64);
+  return {static_cast<int>(std::max<int64_t>(1, (K + len - 1) / len)), static_cast<int>(len)};
+}
+
 struct LoraArgs : GemmArgs {
   const int32_t* adapter;  // INT32[M]
-  uint16_t* h;             // [M][2 * pad]
+  const uint16_t* h;       // [M][2 * pad]
   const uint16_t* up;      // adapter g's N rows of rank elements at g * stride_up
   int64_t ld_up, stride_up;
   int adapters;            // G
@@ -28,17 +47,36 @@ struct LoraArgs : GemmArgs {
 
 typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
-// Elements k .. k+7 of a BF16 row of K at any alignment; zeros past its end (what lies
-// there belongs to another row).
+// Elements k .. k+7 (k a multiple of 8) of a BF16 row of K at any alignment; zeros
+// past its end (what lies there belongs to another row). Without a branch, so that loads of many chunks are in flight together: a chunk
+// that the row's end cuts is the row's last eight elements shifted, one past it the
+// same made zero. Only rows shorter than that are read element by element.
 __device__ __forceinline__ i32x4 load8(const uint16_t* row, int k, int K) {
-  i32x4 v = {0, 0, 0, 0};
-  if (k + 8 <= K) {
-    v = *reinterpret_cast<const i32x4_any*>(row + k);
-  } else if (k < K) {
+  if (K < 8) {
+    i32x4 v = {0, 0, 0, 0};
 #pragma unroll
     for (int q = 0; q < 7; ++q)
       if (k + q < K) v[q >> 1] |= static_cast<int>(static_cast<uint32_t>(row[k + q]) << (16 * (q & 1)));
+    return v;
   }
+  i32x4 v = *reinterpret_cast<const i32x4_any*>(row + min(k, K - 8));
+  if ((K & 7) != 0) {  // the same for the whole launch
+    i32x4 c = v;       // shifted down by 8 - K % 8 elements
+    const int over = 8 - (K & 7);
+    if (over & 4) c = i32x4{c[2], c[3], 0, 0};
+    if (over & 2) c = i32x4{c[1], c[2], c[3], 0};
+    if (over & 1)
+      c = i32x4{static_cast<int>(__builtin_amdgcn_alignbyte(c[1], c[0], 2)),
+                static_cast<int>(__builtin_amdgcn_alignbyte(c[2], c[1], 2)),
+                static_cast<int>(__builtin_amdgcn_alignbyte(c[3], c[2], 2)),
+                static_cast<int>(static_cast<uint32_t>(c[3]) >> 16)};
+    const bool cut = k + 8 > K;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = cut ? c[q] : v[q];
+  }
+  const bool in = k < K;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = in ? v[q] : 0;
   return v;
 }
 
@@ -49,8 +87,11 @@ struct LoraDownArgs {
   const uint16_t* down;
   int64_t ld_down, stride_down;
   const float* scale;  // or nullptr: ones
-  uint16_t* h;
+  uint16_t* h;         // [M][2 * pad]
+  float* partial;      // [shares][M][pad] where shares > 1
   int M, K, adapters, rank, pad;
+  int shares, share_len;
+  int split;           // workgroups that a tile's adapters are dealt to (set by the launch)
 };
 
 hipError_t launch_lora_down(const LoraDownArgs& a, hipStream_t stream);
