@@ -28,6 +28,7 @@
 
 #include "common.hpp"
 #include "internal.hpp"
+#include "lora.hpp"
 
 namespace g355 {
 
@@ -93,8 +94,82 @@ __device__ __forceinline__ void skinny_epilogue(const GemmArgs& p,
   }
 }
 
-template <int TY, int MB, int KW, int U, int OUT>
-__global__ void __launch_bounds__(KW * 64) gemm_skinny_kernel(GemmArgs p) {
+// ------------------------------------------------------------ low-rank adapters
+//
+// At most 16 rows have at most 16 adapters: each wave of a workgroup takes one, and
+// multiplies its h (lora.hpp) with its columns of the workgroup's block on the
+// same MFMA, 32 ranks at a time. What it leaves in LDS for the rows of its adapter is
+// added to their sums after the waves' parts are: in one place whoever shares
+// the batch, so that a row's bits do not depend on its neighbours, and apart from the other rows, so
+// that an adapter's infinities and NaN do not reach them.
+struct WaveAdapter {
+  int g;          // this wave's adapter, or -1
+  unsigned rows;  // its rows
+  unsigned all;   // rows that have an adapter
+};
+
+__device__ __forceinline__ WaveAdapter wave_adapter(const LoraArgs& p, int wave, int lane) {
+  const int m = lane & 15;
+  int id = m < p.M ? p.adapter[m] : -1;
+  id = id < p.adapters ? id : -1;
+  unsigned left = static_cast<unsigned>(__ballot(id >= 0)) & 0xffffu;
+  WaveAdapter a{-1, 0u, left};
+  for (int i = 0; left != 0; ++i) {
+    const int g = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+    const unsigned rows = static_cast<unsigned>(__ballot(id == g)) & 0xffffu;
+    left &= ~rows;
+    if (i == wave) {
+      a.g = g;
+      a.rows = rows;
+    }
+  }
+  return a;
+}
+
+// The lane's part of h's fragments of ranks r .. r + 31 (r + 8 (lane / 16) .. + 7 of row
+// lane % 16), the shares of K added up in their order. Rows without an adapter hold anything.
+__device__ __forceinline__ void h_fragments(const LoraArgs& p, int r, int lane, i32x4& high, i32x4& low) {
+  const int at = r + 8 * (lane >> 4);
+  high = low = i32x4{0, 0, 0, 0};
+  if (at >= p.pad) return;
+  const float* h = p.partial + static_cast<int64_t>(min(lane & 15, p.M - 1)) * p.pad + at;
+  const int64_t next = static_cast<int64_t>(p.M) * p.pad;
+  f32x4 v[2] = {*reinterpret_cast<const f32x4*>(h), *reinterpret_cast<const f32x4*>(h + 4)};
+#pragma unroll 3
+  for (int s = 1; s < p.shares; ++s)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) v[q] += *reinterpret_cast<const f32x4*>(h + s * next + 4 * q);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t h0, l0, h1, l1;
+    split_h(v[q >> 1][2 * (q & 1)], h0, l0);
+    split_h(v[q >> 1][2 * (q & 1) + 1], h1, l1);
+    high[q] = static_cast<int>(h0 | h1 << 16);
+    low[q] = static_cast<int>(l0 | l1 << 16);
+  }
+}
+
+__device__ __forceinline__ f32x4 adapter_mfma(const i32x4& high, const i32x4& low, const i32x4& up, f32x4 d) {
+  d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, high), __builtin_bit_cast(bf16x8_t, up), d,
+                                              0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, low), __builtin_bit_cast(bf16x8_t, up),
+                                                 d, 0, 0, 0);
+}
+
+// d of the adapter's rows to delta[row][column].
+__device__ __forceinline__ void store_delta(const WaveAdapter& a, const f32x4& d, float (&delta)[16][16], int lane) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int row = 4 * (lane >> 4) + e;
+    if ((a.rows >> row) & 1) delta[row][lane & 15] = d[e];
+  }
+}
+
+template <bool LORA>
+using SkinnyArgs = std::conditional_t<LORA, LoraArgs, GemmArgs>;
+
+template <int TY, int MB, int KW, int U, int OUT, bool LORA = false>
+__global__ void __launch_bounds__(KW * 64) gemm_skinny_kernel(SkinnyArgs<LORA> p) {
   using S = SkinnyCfg<TY, MB, KW, U>;
   using Acc = typename S::Acc;
   __shared__ __attribute__((aligned(16))) Acc red[KW][MB][64];
@@ -165,6 +240,27 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_kernel(GemmArgs p) {
     }
   }
 
+  __shared__ float delta[LORA ? 16 : 1][16];
+  unsigned adapted = 0;  // rows that delta holds
+  if constexpr (LORA) {
+    static_assert(MB == 1 && KW >= 16 && TY == TY_BF16, "a wave for every adapter");
+    if (p.adapters > 0) {
+      const WaveAdapter a = wave_adapter(p, __builtin_amdgcn_readfirstlane(wave), lane);
+      adapted = a.all;
+      if (a.g >= 0) {
+        const uint16_t* up = p.up + a.g * p.stride_up + nb * p.ld_up;
+        f32x4 d = {0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < p.pad; r += 32) {
+          const i32x4 columns = load8(up, r + 8 * (lane >> 4), p.rank);
+          i32x4 high, low;
+          h_fragments(p, r, lane, high, low);
+          d = adapter_mfma(high, low, columns, d);
+        }
+        store_delta(a, d, delta, lane);
+      }
+    }
+  }
+
   // Fixed-order reduction of the KW partial sums.
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb) red[wave][mb][lane] = acc[mb];
@@ -175,6 +271,13 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_kernel(GemmArgs p) {
     Acc s = red[0][mb][lane];
 #pragma unroll
     for (int w = 1; w < KW; ++w) s += red[w][mb][lane];
+    if constexpr (LORA) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = 4 * (lane >> 4) + e;
+        if ((adapted >> row) & 1) s[e] += delta[row][lane & 15];
+      }
+    }
     acc[mb] = s;
   }
   const int act = p.act;
@@ -204,8 +307,8 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_kernel(GemmArgs p) {
 template <int TY>
 constexpr bool kSplitLastRound = TY == TY_BF16;
 
-template <int TY, int KW, int KSM, int NBUF, int OUT, int ACT>
-__global__ void __launch_bounds__(KW * 64) gemm_skinny_stream_kernel(GemmArgs p) {
+template <int TY, int KW, int KSM, int NBUF, int OUT, int ACT, bool LORA = false>
+__global__ void __launch_bounds__(KW * 64) gemm_skinny_stream_kernel(SkinnyArgs<LORA> p) {
   using S = SkinnyCfg<TY, 1, KW, 1>;
   using Acc = typename S::Acc;
   constexpr bool FP8 = TY == TY_FP8;
@@ -242,14 +345,23 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_stream_kernel(GemmArgs p)
     return v;
   };
 
-  // A: rows 0..15 (rows past M are zero lanes, never stored).
+  // A: rows 0..15 (rows past M are zero lanes, never stored). With adapters, whose
+  // columns need registers too, three quarters wait in LDS (in registers the kernel
+  // spilled: 16 rows, N = 18432, K = 4096: 64 us).
+  constexpr int IN_LDS = LORA ? 3 * KSM / 4 : 0;
+  __shared__ __attribute__((aligned(16))) Frag a_parts[LORA ? KW : 1][LORA ? IN_LDS : 1][LORA ? 64 : 1];
   Frag av[KSM];
   {
     const int m = lane & 15;
     const bool ok = m < p.M;
     const char* arow = static_cast<const char*>(p.A) + static_cast<int64_t>(ok ? m : 0) * p.lda * S::ES;
 #pragma unroll
-    for (int ks = 0; ks < KSM; ++ks) av[ks] = ld(arow, kb + ks * S::KSTEP, ok && ks < per);
+    for (int ks = 0; ks < KSM; ++ks) {
+      av[ks] = ld(arow, kb + ks * S::KSTEP, ok && ks < per);
+      if constexpr (LORA) {
+        if (ks < IN_LDS) a_parts[wave][ks][lane] = av[ks];
+      }
+    }
   }
   // Work item i of this workgroup: its column range [col0, col0 + width).
   // Items 0..R-1 are the whole blocks blockIdx.x + i G; item R is its share
@@ -291,6 +403,19 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_stream_kernel(GemmArgs p)
     for (int ks = 0; ks < KSM; ++ks) bv[ks] = ld(brow, kb + ks * S::KSTEP, in && ks < per);
   };
 
+  // Adapters of up to 32 ranks: h's two fragments wait in LDS.
+  __shared__ float delta[LORA ? 2 : 1][16][16];
+  __shared__ __attribute__((aligned(16))) i32x4 h_parts[2][LORA ? 64 : 1];
+  WaveAdapter adapter{-1, 0u, 0u};
+  if constexpr (LORA) {
+    static_assert(KW >= 16 && TY == TY_BF16, "a wave for every adapter");
+    if (p.adapters > 0) {
+      adapter = wave_adapter(p, wave, lane);
+      if (wave == 0) h_fragments(p, 0, lane, h_parts[0][lane], h_parts[1][lane]);
+    }
+    __syncthreads();
+  }
+
   Frag bv[NBUF][KSM];
 #pragma unroll
   for (int u = 0; u < NBUF - 1; ++u) {
@@ -304,6 +429,14 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_stream_kernel(GemmArgs p)
       const int i = i0 + u;
       int col0, width;
       if (!item(i, col0, width)) return;
+      // This block's columns of the adapter, requested ahead of the next block's weights:
+      // loads arrive in order, so that waiting for these leaves those in flight.
+      i32x4 up = {0, 0, 0, 0};
+      if constexpr (LORA) {
+        if (adapter.g >= 0)
+          up = load8_raw(p.up + adapter.g * p.stride_up + min(col0 + (lane & 15), p.N - 1) * p.ld_up,
+                         8 * (lane >> 4), p.rank);
+      }
       int cn, wn;  // prefetch: NBUF - 1 items ahead
       if (item(i + NBUF - 1, cn, wn)) load_block(cn, wn, bv[(u + NBUF - 1) % NBUF]);
       Acc acc = {0, 0, 0, 0};
@@ -312,10 +445,19 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_stream_kernel(GemmArgs p)
         if constexpr (FP8) {
           acc = skinny_mfma<TY>(av[ks], bv[u][ks], acc);
         } else {
-          const Frag a = av[ks], b = bv[u][ks];
+          Frag a = av[ks];
+          if constexpr (LORA) {
+            if (ks < IN_LDS) a = a_parts[wave][ks][lane];
+          }
+          const Frag b = bv[u][ks];
           acc = skinny_mfma<TY>(i32x8{a[0], a[1], a[2], a[3], 0, 0, 0, 0},
                                 i32x8{b[0], b[1], b[2], b[3], 0, 0, 0, 0}, acc);
         }
+      }
+      if constexpr (LORA) {
+        if (adapter.g >= 0)
+          store_delta(adapter, adapter_mfma(h_parts[0][lane], h_parts[1][lane], load8_fix(up, 8 * (lane >> 4), p.rank),
+                                            f32x4{0.f, 0.f, 0.f, 0.f}), delta[i & 1], lane);
       }
       red[i & 1][wave][lane] = acc;
       __syncthreads();
@@ -328,6 +470,9 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_stream_kernel(GemmArgs p)
           auto sum = red[i & 1][0][src][r & 3];
 #pragma unroll
           for (int w = 1; w < KW; ++w) sum += red[i & 1][w][src][r & 3];
+          if constexpr (LORA) {
+            if ((adapter.all >> r) & 1) sum += delta[i & 1][r][c];
+          }
           float z = skinny_sum(p, sum, r, n);
           if constexpr (S::ES == 1) z = z * (p.scale_a[r] * p.scale_b[n]);
           z = p.alpha * z;
@@ -410,6 +555,31 @@ hipError_t launch_skinny(const Plan& plan, const LaunchSpec& spec, const GemmArg
   return spec.i8    ? launch_mb<TY_I8, 1>(a, spec.out, stream)
          : spec.fp8 ? launch_mb<TY_FP8, 1>(a, spec.out, stream)
                     : launch_mb<TY_BF16, 1>(a, spec.out, stream);
+}
+
+// The product with adapters, M <= 16: the streaming kernel holds one fragment of ranks
+// (32), the other any number (16 rows, N = 18432, K = 4096: @@ us, tiles of 64 rows and
+// their reduction 45).
+template <int OUT>
+static hipError_t launch_skinny_lora_out(const LoraArgs& a, hipStream_t stream) {
+  constexpr int KW = 16, KSM = 8, NBUF = 2;
+  if (skinny_streams(a.K) && a.pad <= 32) {
+    const dim3 grid(static_cast<unsigned>(skinny_stream_grid(a.N))), block(KW * 64);
+    const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
+    if (a.act == ACT_NONE) go(gemm_skinny_stream_kernel<TY_BF16, KW, KSM, NBUF, OUT, ACT_NONE, true>);
+    else if (a.act == ACT_RELU) go(gemm_skinny_stream_kernel<TY_BF16, KW, KSM, NBUF, OUT, ACT_RELU, true>);
+    else if (a.act == ACT_GELU_ERF) go(gemm_skinny_stream_kernel<TY_BF16, KW, KSM, NBUF, OUT, ACT_GELU_ERF, true>);
+    else go(gemm_skinny_stream_kernel<TY_BF16, KW, KSM, NBUF, OUT, ACT_GELU_TANH, true>);
+  } else {
+    hipLaunchKernelGGL((gemm_skinny_kernel<TY_BF16, 1, KW, 4, OUT, true>), dim3(static_cast<unsigned>((a.N + 15) / 16)),
+                       dim3(KW * 64), 0, stream, a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_skinny_lora(const LaunchSpec& spec, const LoraArgs& a, hipStream_t stream) {
+  if (a.M > 16) return hipErrorInvalidValue;  // the caller only selects M <= 16
+  return spec.out == OUT_BF16 ? launch_skinny_lora_out<OUT_BF16>(a, stream) : launch_skinny_lora_out<OUT_F32>(a, stream);
 }
 #endif  // G355_KERNELS_ONLY
 

@@ -23,12 +23,15 @@ constexpr int64_t k2G = int64_t{1} << 31;
 bool bad_dim(int64_t v) { return v < 0 || v > kMaxDim; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Rows up to which the kernels for few rows (gemm_skinny.hip) are used.
+constexpr int64_t kFewRows = 16;
+
 // The workspace: h, its partial sums, the product's partial sums of a split K.
 size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
 size_t h_bytes(int64_t M, int64_t R) { return rounded(static_cast<size_t>(M) * 4 * padded_rank(R)); }
 size_t partial_bytes(int64_t M, int64_t K, int64_t R) {
   const int shares = lora_shares(M, K, R).shares;
-  return shares == 1 ? 0 : rounded(static_cast<size_t>(shares) * M * padded_rank(R) * sizeof(float));
+  return shares == 1 && M > kFewRows ? 0 : rounded(static_cast<size_t>(shares) * M * padded_rank(R) * sizeof(float));
 }
 
 }  // namespace
@@ -105,12 +108,17 @@ gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R
   a.tiles_n = static_cast<int>((N + plan.bn - 1) / plan.bn);
   a.adapter = adapter;
   a.h = static_cast<const uint16_t*>(workspace);
+  a.partial = reinterpret_cast<const float*>(static_cast<char*>(workspace) + h_bytes(M, R));
+  const LoraShares shares = lora_shares(M, K, R);
+  a.shares = shares.shares;
   a.up = static_cast<const uint16_t*>(up);
   a.ld_up = ld_up;
   a.stride_up = stride_up;
   a.adapters = adapters ? static_cast<int>(G) : 0;
   a.rank = static_cast<int>(R);
   a.pad = static_cast<int>(padded_rank(R));
+  // The kernels for few rows read rows of 16 bytes at a time.
+  const bool few = M <= kFewRows && K % 8 == 0 && lda % 8 == 0 && ldb % 8 == 0 && aligned(A, 16) && aligned(B, 16);
   (void)hipGetLastError();  // an earlier call's pending error is not this call's
   if (adapters) {
     LoraDownArgs d{};
@@ -121,8 +129,7 @@ gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R
     d.ld_down = ld_down;
     d.stride_down = stride_down;
     d.scale = scale;
-    const LoraShares shares = lora_shares(M, K, R);
-    d.h = static_cast<uint16_t*>(workspace);
+    d.h = few ? nullptr : static_cast<uint16_t*>(workspace);
     d.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + h_bytes(M, R));
     d.shares = shares.shares;
     d.share_len = shares.len;
@@ -138,6 +145,8 @@ gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R
   spec.loader_a = spec.loader_b = LOAD_DIRECT;
   spec.out = c_dtype == GEMM_OUT_F32 ? OUT_F32 : OUT_BF16;
   spec.ragged = K % 8 != 0;
+  if (few)
+    return launch_skinny_lora(spec, a, s) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
   if (launch_lora(plan, spec, a, s) != hipSuccess) return GEMM_ERR_HIP;
   if (plan.split > 1 && launch_splitk_reduce(plan, spec, a, s) != hipSuccess) return GEMM_ERR_HIP;
   return GEMM_OK;

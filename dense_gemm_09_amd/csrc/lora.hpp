@@ -16,8 +16,9 @@ inline int64_t padded_rank(int64_t R) { return (R + 15) / 16 * 16; }
 
 // The first factors' product h[m] = scale[a] * (A[m] down_a) of row m with adapter a.
 // It is summed in FP32, over shares of K where that brings more workgroups, and
-// handed to the second factors as two BF16 values: pad high parts RNE(h), then
-// pad low parts RNE(h - high). Off by at most 2^-16 of h, where one BF16 value would be
+// multiplied with the second factors as two BF16 values, high = RNE(h) and
+// low = RNE(h - high): for tiles, which read it often, a row is stored as pad high parts,
+// then pad low ones; the kernels for few rows add up the shares themselves. Off by at most 2^-16 of h, where one BF16 value would be
 // off by 2^-8: as much as the output's own rounding, before it. Columns from the
 // rank on are zeros; rows without an adapter are not written.
 struct LoraShares {
@@ -38,7 +39,9 @@ inline LoraShares lora_shares(int64_t M, int64_t K, int64_t R) {
 
 struct LoraArgs : GemmArgs {
   const int32_t* adapter;  // INT32[M]
-  const uint16_t* h;       // [M][2 * pad]
+  const uint16_t* h;       // [M][2 * pad], tile kernels
+  const float* partial;    // [shares][M][pad], kernels for few rows
+  int shares;
   const uint16_t* up;      // adapter g's N rows of rank elements at g * stride_up
   int64_t ld_up, stride_up;
   int adapters;            // G
@@ -48,10 +51,12 @@ struct LoraArgs : GemmArgs {
 typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
 // Elements k .. k+7 (k a multiple of 8) of a BF16 row of K at any alignment; zeros
-// past its end (what lies there belongs to another row). Without a branch, so that loads of many chunks are in flight together: a chunk
-// that the row's end cuts is the row's last eight elements shifted, one past it the
-// same made zero. Only rows shorter than that are read element by element.
-__device__ __forceinline__ i32x4 load8(const uint16_t* row, int k, int K) {
+// past its end (what lies there belongs to another row). Without a branch, so that
+// loads of many chunks are in flight together: a chunk that the row's end cuts is
+// the row's last eight elements shifted, one past it the same made zero. Only rows
+// shorter than that are read element by element. In two steps, for loads that are
+// to stay in flight: load8_raw, and load8_fix where they are used.
+__device__ __forceinline__ i32x4 load8_raw(const uint16_t* row, int k, int K) {
   if (K < 8) {
     i32x4 v = {0, 0, 0, 0};
 #pragma unroll
@@ -59,7 +64,11 @@ __device__ __forceinline__ i32x4 load8(const uint16_t* row, int k, int K) {
       if (k + q < K) v[q >> 1] |= static_cast<int>(static_cast<uint32_t>(row[k + q]) << (16 * (q & 1)));
     return v;
   }
-  i32x4 v = *reinterpret_cast<const i32x4_any*>(row + min(k, K - 8));
+  return *reinterpret_cast<const i32x4_any*>(row + min(k, K - 8));
+}
+
+__device__ __forceinline__ i32x4 load8_fix(i32x4 v, int k, int K) {
+  if (K < 8) return v;
   if ((K & 7) != 0) {  // the same for the whole launch
     i32x4 c = v;       // shifted down by 8 - K % 8 elements
     const int over = 8 - (K & 7);
@@ -80,6 +89,15 @@ __device__ __forceinline__ i32x4 load8(const uint16_t* row, int k, int K) {
   return v;
 }
 
+__device__ __forceinline__ i32x4 load8(const uint16_t* row, int k, int K) { return load8_fix(load8_raw(row, k, K), k, K); }
+
+// high and low of h (above). Beyond BF16's range low is left out: the difference would be NaN.
+__device__ __forceinline__ void split_h(float h, uint32_t& high, uint32_t& low) {
+  high = f32_to_bf16_bits(h);
+  const float rest = h - bf16_bits_to_f32(static_cast<uint16_t>(high));
+  low = (high & 0x7f80u) == 0x7f80u ? 0u : f32_to_bf16_bits(rest);
+}
+
 struct LoraDownArgs {
   const uint16_t* A;
   int64_t lda;
@@ -87,8 +105,8 @@ struct LoraDownArgs {
   const uint16_t* down;
   int64_t ld_down, stride_down;
   const float* scale;  // or nullptr: ones
-  uint16_t* h;         // [M][2 * pad]
-  float* partial;      // [shares][M][pad] where shares > 1
+  uint16_t* h;         // [M][2 * pad], or nullptr: partial sums are all that is wanted
+  float* partial;      // [shares][M][pad] (not used for one share and an h)
   int M, K, adapters, rank, pad;
   int shares, share_len;
   int split;           // workgroups that a tile's adapters are dealt to (set by the launch)
@@ -100,5 +118,7 @@ struct Plan;
 struct LaunchSpec;
 // The projection's kernel, or its partial sums' (plan.split > 1).
 hipError_t launch_lora(const Plan& plan, const LaunchSpec& spec, const LoraArgs& args, hipStream_t stream);
+// The same for at most 16 rows (gemm_skinny.hip): operands as for launch_skinny.
+hipError_t launch_skinny_lora(const LaunchSpec& spec, const LoraArgs& args, hipStream_t stream);
 
 }  // namespace g355
