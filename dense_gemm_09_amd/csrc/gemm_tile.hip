@@ -743,7 +743,7 @@ using ArgsOf = std::conditional_t<MODE == MODE_LORA, LoraArgs, GemmArgs>;
 // What the adapters need after the main loop must not cost the 128x128 tile the
 // second workgroup on a CU.
 #if defined(G355_LORA)
-#define G355_WAVES_PER_SIMD __attribute__((amdgpu_waves_per_eu(C::BM == 128 ? 2 : 1)))
+#define G355_WAVES_PER_SIMD __attribute__((amdgpu_waves_per_eu(C::BM == 128 && C::KG == 1 ? 2 : 1)))
 #else
 #define G355_WAVES_PER_SIMD
 #endif
@@ -1612,6 +1612,9 @@ hipError_t G355_LORA_LAUNCHER(G355_RAGGED, G355_PART)(const Plan& plan, const Lo
     return plan.bn == 256 ? launch_lora_cfg<Thin16>(plan, a, stream) : launch_lora_cfg<Narrow16>(plan, a, stream);
   if (plan.bm == 256 && plan.bn == 256) return launch_lora_cfg<Big16>(plan, a, stream);
   if (plan.bm == 256) return launch_lora_cfg<Mid16>(plan, a, stream);
+  if constexpr (PART != PART_SPLIT) {
+    if (plan.grid <= kDeepGrid) return launch_lora_cfg<Deep16>(plan, a, stream);
+  }
   return launch_lora_cfg<Small16>(plan, a, stream);
 }
 

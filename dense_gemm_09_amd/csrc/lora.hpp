@@ -31,7 +31,7 @@ constexpr int64_t kLoraWorkgroups = 256;
 
 inline LoraShares lora_shares(int64_t M, int64_t K, int64_t R) {
   const int64_t units = (M + 15) / 16 * std::max<int64_t>(1, padded_rank(R) / 16);
-  const int64_t most = M > 64 ? 1 : std::min<int64_t>(4, std::max<int64_t>(1, kLoraWorkgroups / units));
+  const int64_t most = std::min<int64_t>(4, std::max<int64_t>(1, kLoraWorkgroups / units));
   const int64_t shares = std::max<int64_t>(1, std::min(most, (K + 1023) / 1024));
   const int64_t len = std::max<int64_t>(64, ((K + shares - 1) / shares + 63) / 64 * 64);
   return {static_cast<int>(std::max<int64_t>(1, (K + len - 1) / len)), static_cast<int>(len)};
