@@ -77,10 +77,40 @@ __device__ __forceinline__ int wave_max(int v) {
   return wave_fold(v, INT32_MIN, [](int a, int b) { return max(a, b); });
 }
 
+// The same for doubles.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_f64(double idle, double v) {
+  const uint64_t a = __builtin_bit_cast(uint64_t, idle), b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(static_cast<int>(a), static_cast<int>(b), CTRL, ROWS, 0xf, false);
+  const uint32_t hi =
+      __builtin_amdgcn_update_dpp(static_cast<int>(a >> 32), static_cast<int>(b >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+__device__ __forceinline__ double lane_f64(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), lane);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+template <class F>
+__device__ __forceinline__ double wave_fold(double v, double idle, F combine) {
+  v = combine(v, dpp_f64<0x111, 0xf>(idle, v));
+  v = combine(v, dpp_f64<0x112, 0xf>(idle, v));
+  v = combine(v, dpp_f64<0x114, 0xf>(idle, v));
+  v = combine(v, dpp_f64<0x118, 0xf>(idle, v));
+  v = combine(v, dpp_f64<0x142, 0xa>(idle, v));
+  v = combine(v, dpp_f64<0x143, 0xc>(idle, v));
+  return lane_f64(v, 63);
+}
+
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  return wave_fold(v, 0.0, [](double a, double b) { return a + b; });
+}
+
+__device__ __forceinline__ double wave_max(double v) {
+  return wave_fold(v, -__builtin_inf(), [](double a, double b) { return a > b ? a : b; });
 }
 
 // Floats as integers in the same order (-0 below +0: the callers add 0 first),
@@ -92,18 +122,25 @@ constexpr int kNoKey = static_cast<int>(0x807fffffu);  // key_of(-inf)
 
 __device__ __forceinline__ float wave_top(float v) { return value_of(wave_max(key_of(v))); }
 
-// The largest value of a wave's lanes and the lowest index that has it.
-__device__ __forceinline__ void wave_best(double& v, int& at) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const double u = __shfl_xor(v, o);
-    const int b = __shfl_xor(at, o);
-    if (u > v || (u == v && b < at)) {
-      v = u;
-      at = b;
-    }
+// Keys to choose by: integers in the order of FP32 values, or 64-bit scores.
+template <class Key>
+struct KeyOf;
+template <>
+struct KeyOf<int> {
+  using Score = float;
+  __device__ static constexpr int none() { return kNoKey; }
+  __device__ __forceinline__ static float score(int k) { return value_of(k); }
+  __device__ __forceinline__ static float lane(float v, int l) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
   }
-}
+};
+template <>
+struct KeyOf<double> {
+  using Score = double;
+  __device__ static constexpr double none() { return -__builtin_inf(); }
+  __device__ __forceinline__ static double score(double k) { return k; }
+  __device__ __forceinline__ static double lane(double v, int l) { return lane_f64(v, l); }
+};
 
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
@@ -127,130 +164,69 @@ __device__ __forceinline__ float log_sigmoid(float x) { return fminf(x, 0.f) - l
 // and a bias that happens to one token in 700; 64-bit scores for all of them took
 // 98 us for 16384 tokens, this 49.
 
-// One token's choice with scores in 64 bits. id: lane j's expert (-1: none left).
-template <int EPL>
-__device__ __forceinline__ void choose_exactly(const RouteArgs& p, const float (&x)[EPL], const float (&bias)[EPL],
-                                               float base, int lane, int& id) {
-  const double ninf = -__builtin_inf();
-  double c[EPL], all = 1.0;
-  if (!p.sigmoid) {
-    all = 0.0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) all += exp(static_cast<double>(x[i]) - base);
-    all = wave_sum(all);
-  }
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const double xd = x[i];
-    const double v = (p.sigmoid ? 1.0 / (1.0 + exp(-xd)) : exp(xd - base) / all) + bias[i];
-    c[i] = x[i] > -__builtin_inff() && v == v ? v : ninf;
-  }
-  if (p.groups > 1) {
-    const int per = p.E / p.groups;
-    double mine = ninf;  // score of group `lane`
-    for (int g = 0; g < p.groups; ++g) {
-      double total = ninf;
-      int first = -1;
-      for (int b = 0; b < p.group_best; ++b) {
-        double v = ninf;
-        int at = 1 << 30;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          const int e = lane * EPL + i;
-          if (e >= g * per && e < (g + 1) * per && e != first && c[i] > v) {
-            v = c[i];
-            at = e;
-          }
-        }
-        wave_best(v, at);
-        if (v > ninf) total = b == 0 ? v : total + v;
-        first = at;
-      }
-      if (lane == g) mine = total;
-    }
-    int rank = 0;
-    for (int g = 0; g < p.groups; ++g) {
-      const double v = __shfl(mine, g);
-      if (v > mine || (v == mine && g < lane)) ++rank;
-    }
-    const unsigned long long keep = __ballot(lane < p.groups && rank < p.top_groups);
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane * EPL + i;
-      if (e < p.E && !((keep >> (e / per)) & 1)) c[i] = ninf;
-    }
-  }
-  id = -1;
-  for (int j = 0; j < p.top_k; ++j) {
-    double v = ninf;
-    int at = 1 << 30;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      if (c[i] > v) {
-        v = c[i];
-        at = lane * EPL + i;
-      }
-    }
-    wave_best(v, at);
-    if (!(v > ninf)) break;
-    if (lane == j) id = at;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (lane * EPL + i == at) c[i] = ninf;
-  }
-}
-
 // The lane `step` away within 16 lanes, for butterflies: pairs, quads, and then
 // mirrored halves, whose lanes agree by then.
 template <int STEP>
+constexpr int kAcross = STEP == 1 ? 0xb1 : STEP == 2 ? 0x4e : STEP == 4 ? 0x141 : 0x140;
+template <int STEP>
 __device__ __forceinline__ int across(int v) {
-  constexpr int CTRL = STEP == 1 ? 0xb1 : STEP == 2 ? 0x4e : STEP == 4 ? 0x141 : 0x140;
-  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, true);
+  return __builtin_amdgcn_update_dpp(0, v, kAcross<STEP>, 0xf, 0xf, true);
+}
+template <int STEP>
+__device__ __forceinline__ double across(double v) {
+  return dpp_f64<kAcross<STEP>, 0xf>(v, v);
 }
 
+template <class V>
+__device__ __forceinline__ V larger(V a, V b) { return a > b ? a : b; }
+template <class V>
+__device__ __forceinline__ V smaller(V a, V b) { return a > b ? b : a; }
+
 // The scores of the groups, group g's in lane g: the sum of its one or two best
-// keys. In the usual case a group is 2, 4, 8 or 16 lanes whole, which find its two
-// best in a butterfly, all groups at once; otherwise it is one group after another
-// (256 experts in 8 groups, 16384 tokens: 49 us, one after another 57).
-template <int EPL>
-__device__ __forceinline__ float group_scores(const RouteArgs& p, const int (&key)[EPL], int lane) {
+// keys. In the usual case a group is 1, 2, 4, 8 or 16 lanes whole, which find its two
+// best in a butterfly, all groups at once; otherwise it is one group after another.
+template <int EPL, class Key>
+__device__ __forceinline__ typename KeyOf<Key>::Score group_scores(const RouteArgs& p, const Key (&key)[EPL], int lane) {
+  using K = KeyOf<Key>;
+  using Score = typename K::Score;
+  constexpr Key none = K::none();
   const int per = p.E / p.groups, lanes = per / EPL;
-  float mine = -__builtin_inff();
+  Score mine = -__builtin_inff();
   if (lanes * EPL == per && (lanes & (lanes - 1)) == 0 && lanes >= 1 && lanes <= 16) {
-    int a = kNoKey, b = kNoKey;
+    Key a = none, b = none;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      b = max(b, min(a, key[i]));
-      a = max(a, key[i]);
+      b = larger(b, smaller(a, key[i]));
+      a = larger(a, key[i]);
     }
-    const auto join = [&](int a2, int b2) {
-      b = max(max(b, b2), min(a, a2));
-      a = max(a, a2);
+    const auto join = [&](Key a2, Key b2) {
+      b = larger(larger(b, b2), smaller(a, a2));
+      a = larger(a, a2);
     };
     if (lanes > 1) join(across<1>(a), across<1>(b));
     if (lanes > 2) join(across<2>(a), across<2>(b));
     if (lanes > 4) join(across<4>(a), across<4>(b));
     if (lanes > 8) join(across<8>(a), across<8>(b));
-    float total = value_of(a);
-    if (p.group_best == 2 && b != kNoKey) total += value_of(b);
-    const float there = __shfl(total, (lane * lanes) & 63);
+    Score total = K::score(a);
+    if (p.group_best == 2 && b != none) total += K::score(b);
+    const Score there = __shfl(total, (lane * lanes) & 63);
     return lane < p.groups ? there : mine;
   }
   for (int g = 0; g < p.groups; ++g) {
-    int a = kNoKey, b = kNoKey;
+    Key a = none, b = none;
     const int lo = g * per - lane * EPL, hi = lo + per;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int k = i >= lo && i < hi ? key[i] : kNoKey;
-      b = max(b, min(a, k));
-      a = max(a, k);
+      const Key k = i >= lo && i < hi ? key[i] : none;
+      b = larger(b, smaller(a, k));
+      a = larger(a, k);
     }
-    const int best = wave_max(a);
-    float total = value_of(best);
-    if (p.group_best == 2 && best != kNoKey) {
+    const Key best = wave_max(a);
+    Score total = K::score(best);
+    if (p.group_best == 2 && best != none) {
       const int owner = __builtin_ctzll(__ballot(a == best));
-      const int second = wave_max(lane == owner ? b : a);
-      if (second != kNoKey) total += value_of(second);
+      const Key second = wave_max(lane == owner ? b : a);
+      if (second != none) total += K::score(second);
     }
     if (lane == g) mine = total;
   }
@@ -259,13 +235,14 @@ __device__ __forceinline__ float group_scores(const RouteArgs& p, const int (&ke
 
 // Removes the experts outside the best groups from `key`. Returns whether
 // slack leaves the groups in doubt.
-template <int EPL>
-__device__ __forceinline__ bool keep_groups(const RouteArgs& p, int (&key)[EPL], int lane, float slack) {
+template <int EPL, class Key>
+__device__ __forceinline__ bool keep_groups(const RouteArgs& p, Key (&key)[EPL], int lane, float slack) {
+  using K = KeyOf<Key>;
   const int per = p.E / p.groups;
-  const float mine = group_scores<EPL>(p, key, lane);
+  const auto mine = group_scores<EPL, Key>(p, key, lane);
   int rank = 0;
   for (int g = 0; g < p.groups; ++g) {
-    const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), g));
+    const auto v = K::lane(mine, g);
     rank += (v > mine) | ((v == mine) & (g < lane)) ? 1 : 0;
   }
   const bool kept = lane < p.groups && rank < p.top_groups;
@@ -273,13 +250,74 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs& p, int (&key)[EPL],
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = lane * EPL + i;
-    key[i] = (keep >> ((e / per) & 63)) & 1 ? key[i] : kNoKey;  // (past E there is none anyway)
+    key[i] = (keep >> ((e / per) & 63)) & 1 ? key[i] : K::none();  // (past E there is none anyway)
   }
-  if (p.top_groups == p.groups) return false;
-  const float last = -wave_top(kept ? -mine : -__builtin_inff());
-  const float next = wave_top(kept ? -__builtin_inff() : mine);
+  if (slack == 0.f || p.top_groups == p.groups) return false;
+  const float last = -wave_top(kept ? -static_cast<float>(mine) : -__builtin_inff());
+  const float next = wave_top(kept ? -__builtin_inff() : static_cast<float>(mine));
   // (Groups without an expert left are -inf on both sides: inf - inf is NaN, no doubt.)
   return last - next <= 4.f * slack;
+}
+
+// Rounds: slot j's expert goes to lane j's id (-1: none left). With a slack, one round
+// more tells how near the first expert left out is; returns whether the order is in doubt.
+template <int EPL, class Key>
+__device__ __forceinline__ bool choose(const RouteArgs& p, Key (&key)[EPL], int lane, float slack, int& id) {
+  using K = KeyOf<Key>;
+  bool doubt = false;
+  auto before = K::score(K::none());
+  before = -before;
+  const int rounds = slack > 0.f ? p.top_k + 1 : p.top_k;
+  id = -1;
+  for (int j = 0; j < rounds; ++j) {
+    Key v = key[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) v = larger(v, key[i]);
+    const Key best = wave_max(v);
+    if (best == K::none()) break;
+    const int owner = __builtin_ctzll(__ballot(v == best));
+    // The lowest element of the owner's that has it.
+    int at = EPL - 1;
+#pragma unroll
+    for (int i = EPL - 2; i >= 0; --i)
+      if ((__ballot(key[i] == best) >> owner) & 1) at = i;
+    if (slack > 0.f) {
+      const auto here = K::score(best);
+      doubt |= before - here <= 2.f * slack;
+      before = here;
+    }
+    id = lane == j ? owner * EPL + at : id;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = (lane == owner) & (i == at) ? K::none() : key[i];
+  }
+  if (lane >= p.top_k) id = -1;
+  return doubt;
+}
+
+// One token's choice with scores in 64 bits.
+template <int EPL>
+__device__ __forceinline__ void choose_exactly(const RouteArgs& p, const float (&x)[EPL], const float (&bias)[EPL],
+                                               float base, int lane, int& id) {
+  const double ninf = -__builtin_inf();
+  double c[EPL], all = 1.0;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const double xd = x[i];
+    c[i] = exp(p.sigmoid ? -xd : xd - base);
+  }
+  if (!p.sigmoid) {
+    all = 0.0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) all += c[i];
+    all = wave_sum(all);
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const double v = (p.sigmoid ? 1.0 / (1.0 + c[i]) : c[i] / all) + bias[i];
+    c[i] = x[i] > -__builtin_inff() && v == v ? v : ninf;
+  }
+  if (p.groups > 1) keep_groups<EPL, double>(p, c, lane, 0.f);
+  choose<EPL, double>(p, c, lane, 0.f, id);
 }
 
 // SCORED: keys are scores (a bias, or groups by two scores), not logits.
@@ -357,34 +395,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
         slack = (p.sigmoid ? 0x1p-20f : 0x1p-19f * inverse) + 0x1p-22f * wave_top(most);
       }
       bool doubt = false;
-      if (p.groups > 1) doubt = keep_groups<EPL>(p, key, lane, slack);
-
-      // Rounds: slot j's expert goes to lane j. One round more tells how near the
-      // first expert left out is.
-      float before = __builtin_inff();
-      const int rounds = SCORED ? p.top_k + 1 : p.top_k;
-      for (int j = 0; j < rounds; ++j) {
-        int v = key[0];
-#pragma unroll
-        for (int i = 1; i < EPL; ++i) v = max(v, key[i]);
-        const int best = wave_max(v);
-        if (best == kNoKey) break;
-        const int owner = __builtin_ctzll(__ballot(v == best));
-        // The lowest element of the owner's that has it.
-        int at = EPL - 1;
-#pragma unroll
-        for (int i = EPL - 2; i >= 0; --i)
-          if ((__ballot(key[i] == best) >> owner) & 1) at = i;
-        if constexpr (SCORED) {
-          const float here = value_of(best);
-          doubt |= before - here <= 2.f * slack;
-          before = here;
-        }
-        id = lane == j ? owner * EPL + at : id;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) key[i] = (lane == owner) & (i == at) ? kNoKey : key[i];
-      }
-      if (lane >= p.top_k) id = -1;
+      if (p.groups > 1) doubt = keep_groups<EPL, int>(p, key, lane, slack);
+      doubt |= choose<EPL, int>(p, key, lane, slack, id);
       if constexpr (SCORED) {
         if (__any(doubt)) choose_exactly<EPL>(p, x, bias, base, lane, id);
       }
