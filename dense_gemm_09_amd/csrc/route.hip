@@ -429,68 +429,136 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
 
 // ---------------------------------------------------------------- gradient
 
-// One wave per token; lane j has slot j while the slots' gradients are formed,
-// then lanes have neighbouring experts as above. The whole row is written, zeros
-// mostly, which bounds it.
+// What one slot gives its expert's logit, from its logit xj (id -1: no slot). combine(x) sums
+// x over the token's slots, most(x) is the largest of them. base and sum: softmax's
+// (weights as they are only).
+template <class Sum, class Most>
+__device__ __forceinline__ float slot_gradient(const RouteGradArgs& p, int id, float xj, float dw, float base, float sum,
+                                               Sum combine, Most most) {
+  float v = 0.f;
+  if (p.renormalise) {
+    const float ls = p.sigmoid ? log_sigmoid(xj) : xj;
+    const float top = most(id >= 0 ? ls : -__builtin_inff());
+    const float s = id >= 0 && top > -__builtin_inff() ? expf(ls - top) : 0.f;
+    const float z = combine(s);
+    const float share = s > 0.f ? s / z : 0.f;
+    const float mean = combine(id >= 0 ? dw * share : 0.f);
+    v = id >= 0 ? share * (dw - mean) : 0.f;
+    if (p.sigmoid && id >= 0) v *= 1.f / (1.f + expf(xj));
+  } else if (p.sigmoid) {
+    // s (1 - s), both factors to their relative accuracy
+    if (id >= 0) v = dw * expf(log_sigmoid(xj)) * (1.f / (1.f + expf(xj)));
+  } else {
+    v = id >= 0 ? dw * (expf(xj - base) / sum) : 0.f;
+  }
+  return v;
+}
+
+// Sigmoids and renormalised weights: only chosen experts have a gradient, the rest of
+// the row is zeros. A wave takes 64 / KP tokens (KP >= top_k, a power of two), a lane
+// per slot: their rows are cleared first, the slots' gradients formed meanwhile, and
+// stored over the zeros when those have arrived. Slots that name one expert
+// all hold the sum of theirs, in the slots' order. (16384 tokens of 256 experts, 8
+// slots: a wave per token that wrote whole rows 12.5 us, limited by its instructions; this @@.)
+template <int KP, bool BF16>
+__global__ void __launch_bounds__(kThreads) route_grad_chosen_kernel(RouteGradArgs p) {
+  constexpr int TOKENS = 64 / KP, ES = BF16 ? 2 : 4;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int j = lane % KP;
+  const int bytes = p.E * ES;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 64) * TOKENS;
+  for (int64_t t0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 64) + wave) * TOKENS; t0 < p.T; t0 += step) {
+    const int64_t t = t0 + lane / KP;
+    const bool slot = t < p.T && j < p.top_k;
+    int id = -1;
+    float dw = 0.f, xj = -__builtin_inff();
+    if (slot) {
+      id = p.expert[t * p.top_k + j];
+      dw = p.dweight[t * p.top_k + j];
+    }
+    for (int r = 0; r < TOKENS && t0 + r < p.T; ++r) {
+      char* row = static_cast<char*>(p.dlogits) + (t0 + r) * p.ldd * ES;
+      int c = 16 * lane;
+      for (; c + 16 <= bytes; c += 1024) *reinterpret_cast<u32x4_any*>(row + c) = u32x4_any{0u, 0u, 0u, 0u};
+      for (; c < bytes && c < (bytes & ~15) + 16; c += ES) {  // the lane that the row ends in
+        if constexpr (BF16) *reinterpret_cast<uint16_t*>(row + c) = 0;
+        else *reinterpret_cast<float*>(row + c) = 0.f;
+      }
+    }
+    if (id < 0 || id >= p.E) id = -1;
+    if (id >= 0) xj = load_logit<BF16>(p.logits, t * p.ldl + id);
+    dw = id >= 0 ? p.scale * dw : 0.f;
+    const float v = slot_gradient(
+        p, id, xj, dw, 0.f, 1.f,
+        [](float x) {
+#pragma unroll
+          for (int o = 1; o < KP; o <<= 1) x += __shfl_xor(x, o);
+          return x;
+        },
+        [](float x) {
+#pragma unroll
+          for (int o = 1; o < KP; o <<= 1) x = larger(x, __shfl_xor(x, o));
+          return x;
+        });
+    float total = 0.f;
+#pragma unroll
+    for (int q = 0; q < KP; ++q) {
+      const int other = __shfl(id, (lane & ~(KP - 1)) + q);
+      const float add = __shfl(v, (lane & ~(KP - 1)) + q);
+      total += other == id ? add : 0.f;
+    }
+    // The zeros have to be there before the values.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (id >= 0) {
+      if constexpr (BF16) static_cast<uint16_t*>(p.dlogits)[t * p.ldd + id] = f32_to_bf16_bits(total);
+      else static_cast<float*>(p.dlogits)[t * p.ldd + id] = total;
+    }
+  }
+}
+
+// Softmax's weights as they are: every logit has a gradient. A wave per token; lane j
+// has slot j while the slots' gradients are formed, then lanes have neighbouring
+// experts as in the choice.
 template <int EPL, bool BF16>
-__global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs p) {
+__global__ void __launch_bounds__(kThreads) route_grad_all_kernel(RouteGradArgs p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float ninf = -__builtin_inff();
-  const bool full = !p.sigmoid && !p.renormalise;  // every logit has a gradient
   for (int t = blockIdx.x * (kThreads / 64) + wave; t < p.T; t += gridDim.x * (kThreads / 64)) {
     const int64_t row = t * p.ldl;
     int id = -1;
     float dw = 0.f, xj = ninf;
     if (lane < p.top_k) {
       id = p.expert[static_cast<int64_t>(t) * p.top_k + lane];
-      if (id < 0 || id >= p.E) id = -1;
-      if (id >= 0) {
-        dw = p.scale * p.dweight[static_cast<int64_t>(t) * p.top_k + lane];
-        xj = load_logit<BF16>(p.logits, row + id);
-      }
+      dw = p.dweight[static_cast<int64_t>(t) * p.top_k + lane];
     }
+    float x[EPL];
+    load_row<EPL, BF16>(p.logits, row, p.E, lane, x);
+    if (id < 0 || id >= p.E) id = -1;
+    if (id >= 0) xj = load_logit<BF16>(p.logits, row + id);
+    dw = id >= 0 ? p.scale * dw : 0.f;
     const bool none = !__any(id >= 0);
 
-    float x[EPL], base = 0.f, sum = 1.f;
-    if (full) {
-      load_row<EPL, BF16>(p.logits, row, p.E, lane, x);
-      float top = ninf;
+    float top = ninf;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) top = x[i] > top ? x[i] : top;
-      top = wave_top(top);
-      base = top == ninf ? 0.f : top;
-      sum = 0.f;
+    for (int i = 0; i < EPL; ++i) top = x[i] > top ? x[i] : top;
+    top = wave_top(top);
+    const float base = top == ninf ? 0.f : top;
+    float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        x[i] = fast_exp(x[i] - base);
-        sum += x[i];
-      }
-      sum = wave_sum(sum);
+    for (int i = 0; i < EPL; ++i) {
+      x[i] = fast_exp(x[i] - base);
+      sum += x[i];
     }
-
-    float v = 0.f, dot = 0.f;
-    if (p.renormalise) {
-      const float ls = p.sigmoid ? log_sigmoid(xj) : xj;
-      const float most = wave_top(id >= 0 ? ls : ninf);
-      const float s = id >= 0 && most > ninf ? expf(ls - most) : 0.f;
-      const float z = wave_sum(s);
-      const float share = s > 0.f ? s / z : 0.f;
-      const float mean = wave_sum(id >= 0 ? dw * share : 0.f);
-      v = id >= 0 ? share * (dw - mean) : 0.f;
-      if (p.sigmoid && id >= 0) v *= 1.f / (1.f + expf(xj));
-    } else if (p.sigmoid) {
-      // s (1 - s), both factors to their relative accuracy
-      if (id >= 0) v = dw * expf(log_sigmoid(xj)) * (1.f / (1.f + expf(xj)));
-    } else {
-      v = id >= 0 ? dw * (expf(xj - base) / sum) : 0.f;
-      dot = wave_sum(v);
-    }
+    sum = wave_sum(sum);
+    const float v = slot_gradient(p, id, xj, dw, base, sum, [](float u) { return wave_sum(u); },
+                                  [](float u) { return wave_top(u); });
 
     float d[EPL];
-    const float f = full && !none ? -dot / sum : 0.f;
+    const float f = none ? 0.f : -wave_sum(v) / sum;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) d[i] = full && !none ? f * x[i] : 0.f;
+    for (int i = 0; i < EPL; ++i) d[i] = none ? 0.f : f * x[i];
     const int e0 = lane * EPL;
     for (int j = 0; j < p.top_k; ++j) {
       const int at = __builtin_amdgcn_readlane(id, j) - e0;
@@ -555,10 +623,20 @@ hipError_t launch_route(const RouteArgs& a, bool bf16, hipStream_t stream) {
 }
 
 hipError_t launch_route_grad(const RouteGradArgs& a, bool bf16, hipStream_t stream) {
+  if (a.sigmoid || a.renormalise) {
+    const auto run = [&](auto kernel, int kp) {
+      hipLaunchKernelGGL(kernel, token_grid((a.T + 64 / kp - 1) / (64 / kp)), dim3(kThreads), 0, stream, a);
+    };
+    if (a.top_k <= 2) bf16 ? run(route_grad_chosen_kernel<2, true>, 2) : run(route_grad_chosen_kernel<2, false>, 2);
+    else if (a.top_k <= 4) bf16 ? run(route_grad_chosen_kernel<4, true>, 4) : run(route_grad_chosen_kernel<4, false>, 4);
+    else if (a.top_k <= 8) bf16 ? run(route_grad_chosen_kernel<8, true>, 8) : run(route_grad_chosen_kernel<8, false>, 8);
+    else bf16 ? run(route_grad_chosen_kernel<32, true>, 32) : run(route_grad_chosen_kernel<32, false>, 32);
+    return hipGetLastError();
+  }
   const auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, token_grid(a.T), dim3(kThreads), 0, stream, a); };
   with_experts_per_lane(a.E, [&](auto n) {
     constexpr int EPL = decltype(n)::value;
-    bf16 ? run(route_grad_kernel<EPL, true>) : run(route_grad_kernel<EPL, false>);
+    bf16 ? run(route_grad_all_kernel<EPL, true>) : run(route_grad_all_kernel<EPL, false>);
   });
   return hipGetLastError();
 }
