@@ -11,7 +11,9 @@
 // from one row take a third of the time), so that only rows that have the adapter
 // are read, and the reads are spread over the CUs: few rows have shares of K and
 // adapters in workgroups of their own (a launch of more workgroups than that costs more than they
-// bring: about 455 waves start in a microsecond). Measured: 4096 rows, K = 4096, R = 16, @@ us.
+// bring: about 455 waves start in a microsecond). Measured: 4096 rows, K = 4096,
+// R = 16, 18 us; 64 rows of 24 adapters, K = 14336, R = 64, 17 us (44 MB of adapters:
+// 9 us at a copy's rate); one row 4 us.
 
 #include "lora.hpp"
 
@@ -23,6 +25,7 @@ constexpr int kWaves = 8;
 constexpr int kTurn = 64;  // K elements of a wave's turn
 constexpr int kMaxTiles = 1 << 20;
 
+// high and low of one element (lora.hpp).
 __device__ __forceinline__ void store_h(const LoraDownArgs& p, int m, int r, float h) {
   uint16_t* row = p.h + static_cast<int64_t>(m) * 2 * p.pad;
   uint32_t high, low;

@@ -161,8 +161,8 @@ __device__ __forceinline__ float log_sigmoid(float x) { return fminf(x, 0.f) - l
 // FP32, each within `slack` of its exact value; where two neighbours in the order
 // found (or the last group kept and the first not) are closer than that decides,
 // the token is done again with scores in 64 bits. With 256 experts, random logits
-// and a bias that happens to one token in 700; 64-bit scores for all of them took
-// 98 us for 16384 tokens, this 49.
+// and a bias that happens to one token in 700 (16384 tokens: 64-bit scores for all
+// of them 98 us, this 27).
 
 // The lane `step` away within 16 lanes, for butterflies: pairs, quads, and then
 // mirrored halves, whose lanes agree by then.
@@ -320,9 +320,11 @@ __device__ __forceinline__ void choose_exactly(const RouteArgs& p, const float (
   choose<EPL, double>(p, c, lane, 0.f, id);
 }
 
-// SCORED: keys are scores (a bias, or groups by two scores), not logits.
+// SCORED: keys are scores (a bias, or groups by two scores), not logits. Up to 256
+// experts, six waves to a SIMD: the 64-bit scores, rarely needed, would take the
+// registers of one (16384 tokens of 256 experts with gradient: 35.4 us, so 32.5).
 template <int EPL, bool BF16, bool SCORED>
-__global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs p) {
+__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(EPL <= 4 ? 6 : 1))) route_kernel(RouteArgs p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float ninf = -__builtin_inff();
@@ -459,7 +461,7 @@ __device__ __forceinline__ float slot_gradient(const RouteGradArgs& p, int id, f
 // per slot: their rows are cleared first, the slots' gradients formed meanwhile, and
 // stored over the zeros when those have arrived. Slots that name one expert
 // all hold the sum of theirs, in the slots' order. (16384 tokens of 256 experts, 8
-// slots: a wave per token that wrote whole rows 12.5 us, limited by its instructions; this @@.)
+// slots: a wave per token that wrote whole rows 12.5 us, limited by its instructions; this 7.)
 template <int KP, bool BF16>
 __global__ void __launch_bounds__(kThreads) route_grad_chosen_kernel(RouteGradArgs p) {
   constexpr int TOKENS = 64 / KP, ES = BF16 ? 2 : 4;
@@ -593,7 +595,7 @@ __global__ void __launch_bounds__(kThreads) route_grad_all_kernel(RouteGradArgs 
 }
 
 // Workgroups of gemm_route at most: those that are on the card at once.
-constexpr int kRouteGrid = 256 * 5;
+constexpr int kRouteGrid = 256 * 6;
 
 // Experts per lane for E of them.
 template <class Go>

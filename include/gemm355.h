@@ -404,7 +404,9 @@ gemm_status gemm_grouped_bf16_wgrad(int64_t G, int64_t T, int64_t N, int64_t K, 
  * groups that do not divide E, top_groups outside [1, groups], group_best other
  * than 1 or 2, top_k < 1 or above the experts of top_groups groups.
  * GEMM_ERR_BAD_ENUM: l_dtype, score. Then GEMM_ERR_BAD_LD,
- * GEMM_ERR_NULL_POINTER, GEMM_ERR_HIP. T == 0 launches nothing.
+ * GEMM_ERR_NULL_POINTER, GEMM_ERR_UNSUPPORTED (a pointer not aligned to its
+ * elements), GEMM_ERR_HIP. T == 0 launches nothing. expert and weight may not
+ * overlap each other or the inputs.
  */
 typedef enum { GEMM_SCORE_SOFTMAX = 0, GEMM_SCORE_SIGMOID = 1 } gemm_score;
 
@@ -454,8 +456,8 @@ size_t gemm_route_order_workspace_size(int64_t S, int64_t G);
  * X: T rows of N elements of elem_bytes (1, 2 or 4: codes, BF16, FP32 or the
  * scales of codes; moved as bits), ldx >= N. Y: R rows, ldy >= N. Positions
  * outside [0, R) are passed over. Rows of Y that no slot names are not
- * written. A position named twice gets one of its rows.
- * Its gradient is gemm_combine_rows without weights.
+ * written. A position named twice gets one of its rows, or parts of several.
+ * Y may not overlap X. Its gradient is gemm_combine_rows without weights.
  * Errors: GEMM_ERR_BAD_ENUM (elem_bytes), GEMM_ERR_BAD_DIM (a size negative or
  * above 2^30, T * top_k above 2^30, top_k < 1), GEMM_ERR_UNSUPPORTED (top_k above 64, X or Y not
  * aligned to its elements), GEMM_ERR_BAD_LD,
@@ -470,7 +472,7 @@ gemm_status gemm_dispatch_rows(int64_t T, int64_t top_k, int64_t R, int64_t N, c
  *   C[t, :] = sum_j weight[t, j] * Y[position[t * top_k + j], :] + beta * C[t, :]
  * summed in FP32 in the order of j, rounded once. Slots with a position
  * outside [0, R) add nothing, whatever their weight (a token without slots:
- * beta * C). Y: R rows of N, FP32 or BF16, ldy >= N. weight: FP32[T][top_k],
+ * beta * C). C may not overlap Y. Y: R rows of N, FP32 or BF16, ldy >= N. weight: FP32[T][top_k],
  * or NULL for ones. C: T rows, FP32 or BF16, ldc >= N, not read for beta == 0.
  * Errors as for gemm_dispatch_rows; GEMM_ERR_BAD_ENUM for the types. T == 0 or
  * N == 0 launches nothing; R == 0 gives beta * C.
@@ -487,7 +489,8 @@ gemm_status gemm_combine_rows(int64_t T, int64_t top_k, int64_t R, int64_t N, co
  * D: T rows of N, d_dtype, ldd >= N. Y, dY: R rows, y_dtype. weight as above
  * (NULL: ones). dweight: FP32[T][top_k], or NULL: it is not computed and Y,
  * which may be NULL then, not read. Rows of dY that no slot names are not
- * written. dY may not overlap Y. Sums are FP32. Errors as above.
+ * written; a row that several name gets the gradient of one, or parts of several. dY
+ * may not overlap D or Y. Sums are FP32. Errors as above.
  */
 gemm_status gemm_combine_rows_grad(int64_t T, int64_t top_k, int64_t R, int64_t N, const void* D,
                                    int64_t ldd, gemm_out_dtype d_dtype, const void* Y, int64_t ldy,
