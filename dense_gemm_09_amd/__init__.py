@@ -187,25 +187,28 @@ def _need(t, nbytes: int, what: str):
         raise ValueError(f"{what} holds {_nbytes(t)} bytes, the call reads/writes {nbytes}")
 
 
+_dtypes = {}
+
+
+def _dtype(name: str):
+    """torch's data type of that name. (An import in a function costs as much as the check it serves.)"""
+    if name not in _dtypes:
+        import torch
+        _dtypes[name] = getattr(torch, name)
+    return _dtypes[name]
+
+
 def _need_int32(t, n: int, what: str):
     """A vector of n INT32: one of another integer type has the bytes, but is read as other numbers."""
     if t is None or isinstance(t, int) or n <= 0:
         return
-    import torch
-    if t.dtype is not torch.int32:
+    if t.dtype is not _dtype("int32"):
         raise ValueError(f"{what} must be INT32, not {t.dtype}")
     _need(t, 4 * n, what)
 
 
 def _one_device(stream, **tensors):
     """The kernels run on the current device (or the stream's): a tensor elsewhere, on the host too, is refused."""
-    global _device_count
-    if _device_count is None:
-        import torch
-        _device_count = torch.cuda.device_count()
-    if _device_count == 1:
-        # There is no other device, and _need has seen to the host's tensors but for a workspace.
-        tensors = {"workspace": tensors.get("workspace")}
     where = stream.device.index if stream is not None and not isinstance(stream, int) else None
     for what, t in tensors.items():
         if t is None or isinstance(t, int):
@@ -223,12 +226,20 @@ def _one_device(stream, **tensors):
 _device_count = None
 
 
+def _several_devices() -> bool:
+    """Whether a tensor may be on another device. (If not, _need has seen to the host's.)"""
+    global _device_count
+    if _device_count is None:
+        import torch
+        _device_count = torch.cuda.device_count()
+    return _device_count > 1
+
+
 def _need_f32(t, n: int, what: str):
     """A vector of n FP32."""
     if t is None or isinstance(t, int) or n <= 0:
         return
-    import torch
-    if t.dtype is not torch.float32:
+    if t.dtype is not _dtype("float32"):
         raise ValueError(f"{what} must be FP32, not {t.dtype}")
     _need(t, 4 * n, what)
 
@@ -513,7 +524,8 @@ def route(T, E, top_k, logits, ldl, l_dtype, score, bias, groups, top_groups, gr
         _need_f32(bias, E, "bias")
         _need_int32(expert, T * top_k, "expert")
         _need_f32(weight, T * top_k, "weight")
-        _one_device(stream, logits=logits, bias=bias, expert=expert, weight=weight)
+        if _several_devices():
+            _one_device(stream, logits=logits, bias=bias, expert=expert, weight=weight)
     st = L.gemm_route(T, E, top_k, _ptr(logits), ldl, l_dtype, score, _ptr(bias), groups, top_groups, group_best,
                       1 if renormalise else 0, scale, _ptr(expert), _ptr(weight), _stream(stream))
     if st != 0:
@@ -529,7 +541,8 @@ def route_grad(T, E, top_k, logits, ldl, l_dtype, score, renormalise, scale, exp
         _need_int32(expert, T * top_k, "expert")
         _need_f32(dweight, T * top_k, "dweight")
         _need(dlogits, _size(l_dtype) * _extent(T, E, ldd), "dlogits")
-        _one_device(stream, logits=logits, expert=expert, dweight=dweight, dlogits=dlogits)
+        if _several_devices():
+            _one_device(stream, logits=logits, expert=expert, dweight=dweight, dlogits=dlogits)
     st = L.gemm_route_grad(T, E, top_k, _ptr(logits), ldl, l_dtype, score, 1 if renormalise else 0, scale,
                            _ptr(expert), _ptr(dweight), _ptr(dlogits), ldd, _stream(stream))
     if st != 0:
@@ -549,7 +562,8 @@ def route_order(S, G, expert, offsets, position, order=None, workspace=None, wor
         _need_int32(offsets, G + 1, "offsets")
         _need_int32(position, S, "position")
         _need_int32(order, S, "order")
-        _one_device(stream, expert=expert, offsets=offsets, position=position, order=order, workspace=workspace)
+        if workspace is not None or _several_devices():
+            _one_device(stream, expert=expert, offsets=offsets, position=position, order=order, workspace=workspace)
     workspace, workspace_bytes = _scratch(route_order_workspace_size(S, G), workspace, workspace_bytes, stream)
     st = L.gemm_route_order(S, G, _ptr(expert), _ptr(offsets), _ptr(position), _ptr(order), _ptr(workspace),
                             workspace_bytes, _stream(stream))
@@ -564,7 +578,8 @@ def dispatch_rows(T, top_k, R, N, X, ldx, elem_bytes, position, Y, ldy, stream=N
         _need(X, elem_bytes * _extent(T, N, ldx), "X")
         _need_int32(position, T * top_k, "position")
         _need(Y, elem_bytes * _extent(R, N, ldy), "Y")
-        _one_device(stream, X=X, position=position, Y=Y)
+        if _several_devices():
+            _one_device(stream, X=X, position=position, Y=Y)
     st = L.gemm_dispatch_rows(T, top_k, R, N, _ptr(X), ldx, elem_bytes, _ptr(position), _ptr(Y), ldy,
                               _stream(stream))
     if st != 0:
@@ -579,7 +594,8 @@ def combine_rows(T, top_k, R, N, Y, ldy, y_dtype, position, weight, beta, C, ldc
         _need_int32(position, T * top_k, "position")
         _need_f32(weight, T * top_k, "weight")
         _need(C, _size(c_dtype) * _extent(T, N, ldc), "C")
-        _one_device(stream, Y=Y, position=position, weight=weight, C=C)
+        if _several_devices():
+            _one_device(stream, Y=Y, position=position, weight=weight, C=C)
     st = L.gemm_combine_rows(T, top_k, R, N, _ptr(Y), ldy, y_dtype, _ptr(position), _ptr(weight), beta, _ptr(C), ldc,
                              c_dtype, _stream(stream))
     if st != 0:
@@ -599,8 +615,9 @@ def combine_rows_grad(T, top_k, R, N, D, ldd, d_dtype, Y, ldy, y_dtype, position
         _need_int32(position, T * top_k, "position")
         _need_f32(weight, T * top_k, "weight")
         _need_f32(dweight, T * top_k, "dweight")
-        _one_device(stream, D=D, Y=Y if dweight is not None else None, position=position, weight=weight, dY=dY,
-                    dweight=dweight)
+        if _several_devices():
+            _one_device(stream, D=D, Y=Y if dweight is not None else None, position=position, weight=weight, dY=dY,
+                        dweight=dweight)
     st = L.gemm_combine_rows_grad(T, top_k, R, N, _ptr(D), ldd, d_dtype, _ptr(Y), ldy, y_dtype, _ptr(position),
                                   _ptr(weight), _ptr(dY), lddy, _ptr(dweight), _stream(stream))
     if st != 0:
@@ -626,9 +643,11 @@ def gemm_lora_bf16(M, N, K, G, R, alpha, A, lda, B, ldb, adapter, down, ld_down,
         _need(down, 2 * ((G - 1) * stride_down + _extent(R, K, ld_down)) if K > 0 else 0, "down")
         _need(up, 2 * ((G - 1) * stride_up + _extent(N, R, ld_up)), "up")
         _need_f32(scale, G, "scale")
-    if M > 0 and N > 0:
+    if M > 0 and N > 0 and _several_devices():
         _one_device(stream, A=A, B=B, adapter=adapter, down=down, up=up, scale=scale, C=C, bias=bias,
                     workspace=workspace)
+    elif workspace is not None:
+        _one_device(stream, workspace=workspace)
     workspace, workspace_bytes = _scratch(lora_workspace_size(M, N, K, R), workspace, workspace_bytes, stream)
     st = L.gemm_lora_bf16(M, N, K, G, R, alpha, _ptr(A), lda, _ptr(B), ldb, _ptr(adapter), _ptr(down), ld_down,
                           stride_down, _ptr(up), ld_up, stride_up, _ptr(scale), beta, _ptr(C), ldc, c_dtype,
