@@ -1,8 +1,9 @@
 // C ABI of the projection with low-rank adapters: argument validation, plan and dispatch.
 //
-// Two launches (three with a split K): the first factors' product h, and the
-// projection's own kernel, which adds h times the second factors to its
-// accumulators before its epilogue.
+// Two to four launches: the first factors' product h (with the sum of its shares of K
+// where it has several and the tiles run), and the projection's own kernel, which adds
+// h times the second factors to its accumulators before its epilogue (with the
+// reduction of a split K).
 
 #include <hip/hip_runtime.h>
 
