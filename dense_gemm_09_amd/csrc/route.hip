@@ -657,11 +657,6 @@ hipError_t launch_route_grad(const RouteGradArgs& a, bool bf16, hipStream_t stre
 // All of it is latency: a second launch costs more than what it does (32768 slots of 64
 // experts: three launches with a scan of their own took 15 us).
 
-constexpr int kSmallWaves = 16;      // 512 slots a wave, eight to a lane
-constexpr int kOrderWaves = 4;
-constexpr int kHeldKeys = 8;         // keys that a lane holds at a time
-constexpr int kMaxChunks = 128;
-
 __device__ __forceinline__ int expert_key(const OrderArgs& p, int s) {
   const int e = p.expert[s];
   return e >= 0 && e < p.G ? e : p.G;
@@ -804,17 +799,6 @@ __global__ void __launch_bounds__(64 * WAVES) order_place_kernel(OrderArgs p) {
   }
 }
 
-void order_chunks(int64_t S, int64_t G, int& chunk, int& chunks) {
-  if (order_small(S, G)) {
-    chunk = static_cast<int>((S + 64 * kSmallWaves - 1) / (64 * kSmallWaves) * (64 * kSmallWaves));
-    chunks = 1;
-    return;
-  }
-  const int64_t least = 64 * kHeldKeys * kOrderWaves, per = (S + kMaxChunks - 1) / kMaxChunks;
-  chunk = static_cast<int>((per + least - 1) / least * least);
-  chunks = static_cast<int>((S + chunk - 1) / chunk);
-}
-
 hipError_t launch_order(const OrderArgs& a, hipStream_t stream) {
   const size_t lds = static_cast<size_t>(a.G + 1) * sizeof(int);
   if (order_small(a.S, a.G)) {
@@ -822,11 +806,14 @@ hipError_t launch_order(const OrderArgs& a, hipStream_t stream) {
                        stream, a);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(order_count_kernel, dim3(a.chunks), dim3(64 * kOrderWaves), lds, stream, a);
-  const hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
-  hipLaunchKernelGGL((order_place_kernel<kOrderWaves, false>), dim3(a.chunks), dim3(64 * kOrderWaves),
-                     kOrderWaves * lds, stream, a);
+  // Without slots there are no counts (and no workspace): one workgroup writes the offsets.
+  if (a.chunks > 0) {
+    hipLaunchKernelGGL(order_count_kernel, dim3(a.chunks), dim3(64 * kOrderWaves), lds, stream, a);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  hipLaunchKernelGGL((order_place_kernel<kOrderWaves, false>), dim3(a.chunks > 0 ? a.chunks : 1),
+                     dim3(64 * kOrderWaves), kOrderWaves * lds, stream, a);
   return hipGetLastError();
 }
 

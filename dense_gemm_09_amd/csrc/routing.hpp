@@ -4,12 +4,13 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "order_plan.hpp"
+
 namespace g355 {
 
 constexpr int kMaxExperts = 1024;      // logits of a row that the routing kernels hold
 constexpr int kMaxTopK = 32;
 constexpr int kMaxRouteGroups = 64;    // one lane each
-constexpr int kMaxOrderGroups = 8192;  // counters of a workgroup in LDS
 constexpr int kMaxSlots = 64;          // top_k of the row movements (a slot per lane)
 
 // Workgroups of a launch at most (HIP counts a launch's threads in 32 bits);
@@ -53,14 +54,6 @@ struct OrderArgs {
   int chunk, chunks;  // slots per chunk (a multiple of 64 per wave)
 };
 
-// Sorted by one workgroup, which holds the slots' experts in registers and its 16
-// waves' counters in LDS.
-constexpr int kSmallSlots = 8192;
-constexpr int kSmallGroups = 2047;
-inline bool order_small(int64_t S, int64_t G) { return S <= kSmallSlots && G <= kSmallGroups; }
-
-// The division of S slots into chunks.
-void order_chunks(int64_t S, int64_t G, int& chunk, int& chunks);
 hipError_t launch_order(const OrderArgs& a, hipStream_t stream);
 
 struct RowsArgs {
