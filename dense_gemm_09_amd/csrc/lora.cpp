@@ -22,6 +22,12 @@ constexpr int64_t kMaxDim = int64_t{1} << 30;
 constexpr int64_t k2G = int64_t{1} << 31;
 
 bool bad_dim(int64_t v) { return v < 0 || v > kMaxDim; }
+// Whether rows of K BF16 elements, ld apart, span less than 2 GiB. (A product of a
+// leading dimension that nothing bounds is not formed: it may exceed 64 bits.)
+bool under_2g(int64_t rows, int64_t K, int64_t ld) {
+  if (rows > 1 && ld >= k2G / 2 / (rows - 1) + 1) return false;
+  return ((rows - 1) * ld + K) * 2 < k2G;
+}
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Rows up to which the kernels for few rows (gemm_skinny.hip) are used.
@@ -81,7 +87,7 @@ gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R
       !aligned(C, c_dtype == GEMM_OUT_F32 ? 4 : 2))
     return GEMM_ERR_UNSUPPORTED;
   // The copies' 32-bit offsets.
-  if (((M - 1) * lda + K) * 2 >= k2G || ((N - 1) * ldb + K) * 2 >= k2G) return GEMM_ERR_UNSUPPORTED;
+  if (!under_2g(M, K, lda) || !under_2g(N, K, ldb)) return GEMM_ERR_UNSUPPORTED;
 
   Plan plan = make_tile_plan(M, N, K, false);
   // Tiles of 128x128 that the dense product splits in two and that the CUs hold at
