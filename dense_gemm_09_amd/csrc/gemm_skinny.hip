@@ -563,7 +563,7 @@ hipError_t launch_skinny(const Plan& plan, const LaunchSpec& spec, const GemmArg
 template <int OUT>
 static hipError_t launch_skinny_lora_out(const LoraArgs& a, hipStream_t stream) {
   constexpr int KW = 16, KSM = 8, NBUF = 2;
-  if (skinny_streams(a.K) && a.pad <= 32) {
+  if (skinny_streams_lora(a.K, a.pad)) {
     const dim3 grid(static_cast<unsigned>(skinny_stream_grid(a.N))), block(KW * 64);
     const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, stream, a); };
     if (a.act == ACT_NONE) go(gemm_skinny_stream_kernel<TY_BF16, KW, KSM, NBUF, OUT, ACT_NONE, true>);

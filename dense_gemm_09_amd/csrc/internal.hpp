@@ -121,6 +121,8 @@ hipError_t launch_skinny(const Plan& plan, const LaunchSpec& spec, const GemmArg
 // The skinny kernel's streaming variant covers K up to 16 waves x 4096/16
 // elements; its grid is one workgroup per CU at most.
 inline bool skinny_streams(int64_t K) { return K <= 4096; }
+// With adapters it holds one fragment of their ranks (32 of the padded ones) too.
+inline bool skinny_streams_lora(int64_t K, int64_t pad) { return skinny_streams(K) && pad <= 32; }
 inline int64_t skinny_stream_grid(int64_t N) {
   const int64_t blocks = (N + 15) / 16;
   return blocks < 256 ? blocks : 256;

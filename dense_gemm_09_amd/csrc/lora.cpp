@@ -133,8 +133,11 @@ gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R
   a.adapters = adapters ? static_cast<int>(G) : 0;
   a.rank = static_cast<int>(R);
   a.pad = static_cast<int>(padded_rank(R));
-  // The kernels for few rows read rows of 16 bytes at a time.
-  const bool few = M <= kFewRows && K % 8 == 0 && lda % 8 == 0 && ldb % 8 == 0 && aligned(A, 16) && aligned(B, 16);
+  // The kernels for few rows read rows of 16 bytes at a time. The one that does not
+  // stream has a workgroup of 1024 threads for every 16 columns, and HIP counts a launch's
+  // threads in 32 bits: more columns run on tiles.
+  const bool few = M <= kFewRows && K % 8 == 0 && lda % 8 == 0 && ldb % 8 == 0 && aligned(A, 16) && aligned(B, 16) &&
+                   (skinny_streams_lora(K, a.pad) || (N + 15) / 16 < int64_t{1} << 22);
   (void)hipGetLastError();  // an earlier call's pending error is not this call's
   if (adapters) {
     LoraDownArgs d{};
