@@ -86,8 +86,13 @@ gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R
       !aligned(up, 2) || !aligned(A, 2) || !aligned(B, 2) || !aligned(bias, 2) ||
       !aligned(C, c_dtype == GEMM_OUT_F32 ? 4 : 2))
     return GEMM_ERR_UNSUPPORTED;
-  // The copies' 32-bit offsets.
-  if (!under_2g(M, K, lda) || !under_2g(N, K, ldb)) return GEMM_ERR_UNSUPPORTED;
+  // The kernels for few rows read rows of 16 bytes at a time. The one that does not
+  // stream has a workgroup of 1024 threads for every 16 columns, and HIP counts a launch's
+  // threads in 32 bits: more columns run on tiles. They address the weight in 64 bits,
+  // the tiles' copies both operands in 32.
+  const bool few = M <= kFewRows && K % 8 == 0 && lda % 8 == 0 && ldb % 8 == 0 && ldb < k2G && aligned(A, 16) &&
+                   aligned(B, 16) && (skinny_streams_lora(K, padded_rank(R)) || (N + 15) / 16 < int64_t{1} << 22);
+  if (!under_2g(M, K, lda) || (!few && !under_2g(N, K, ldb))) return GEMM_ERR_UNSUPPORTED;
 
   Plan plan = make_tile_plan(M, N, K, false);
   // Tiles of 128x128 that the dense product splits in two and that the CUs hold at
@@ -133,11 +138,6 @@ gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R
   a.adapters = adapters ? static_cast<int>(G) : 0;
   a.rank = static_cast<int>(R);
   a.pad = static_cast<int>(padded_rank(R));
-  // The kernels for few rows read rows of 16 bytes at a time. The one that does not
-  // stream has a workgroup of 1024 threads for every 16 columns, and HIP counts a launch's
-  // threads in 32 bits: more columns run on tiles.
-  const bool few = M <= kFewRows && K % 8 == 0 && lda % 8 == 0 && ldb % 8 == 0 && aligned(A, 16) && aligned(B, 16) &&
-                   (skinny_streams_lora(K, a.pad) || (N + 15) / 16 < int64_t{1} << 22);
   (void)hipGetLastError();  // an earlier call's pending error is not this call's
   if (adapters) {
     LoraDownArgs d{};

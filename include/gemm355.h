@@ -518,7 +518,9 @@ gemm_status gemm_combine_rows_grad(int64_t T, int64_t top_k, int64_t R, int64_t 
  * workspace: gemm_lora_workspace_size(M, N, K, R) bytes, 16-byte aligned.
  * Errors as for gemm_bf16; GEMM_ERR_BAD_LD also for a negative stride_down or
  * stride_up; GEMM_ERR_UNSUPPORTED for R above 128 or G above 65536, A or B that spans
- * 2^31 bytes or more, BF16 operands at odd addresses, a workspace not 16-byte aligned.
+ * 2^31 bytes or more (B may where M <= 16, K is a multiple of 8 and the rows of A and B are
+ * 16-byte aligned; more than 2^26 - 16 columns take K <= 4096 and R <= 32 as well), BF16
+ * operands at odd addresses, a workspace not 16-byte aligned.
  */
 gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R, float alpha,
                            const void* A, int64_t lda, const void* B, int64_t ldb,
