@@ -149,9 +149,10 @@ __device__ __forceinline__ void h_fragments(const LoraArgs& p, int r, int lane, 
   }
 }
 
-__device__ __forceinline__ f32x4 adapter_mfma(const i32x4& high, const i32x4& low, const i32x4& up, f32x4 d) {
+__device__ __forceinline__ f32x4 adapter_mfma(const i32x4& high, const i32x4& low, i32x4 up, f32x4 d) {
   d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, high), __builtin_bit_cast(bf16x8_t, up), d,
                                               0, 0, 0);
+  if (__any(unbounded(up) != 0)) up = bounded(up);
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, low), __builtin_bit_cast(bf16x8_t, up),
                                                  d, 0, 0, 0);
 }

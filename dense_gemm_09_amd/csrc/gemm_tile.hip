@@ -718,14 +718,27 @@ __device__ __forceinline__ void add_adapters(const LoraArgs& p, f32x16 (&acc)[C:
 #pragma unroll
           for (int j = 0; j < C::FN; ++j) u[t][j] = load8(up[j] + at, r + 8 * half, p.rank);
         }
+        uint32_t infinite = 0;
 #pragma unroll
         for (int t = 0; t < TU; ++t)
 #pragma unroll
           for (int j = 0; j < C::FN; ++j) {
-            const bf16x8 b = __builtin_bit_cast(bf16x8, u[t][j]);
-            d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, high[t]), b, d[j], 0, 0, 0);
-            d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, low[t]), b, d[j], 0, 0, 0);
+            infinite |= unbounded(u[t][j]);
+            d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, high[t]),
+                                                           __builtin_bit_cast(bf16x8, u[t][j]), d[j], 0, 0, 0);
           }
+        if (__any(infinite != 0)) {
+#pragma unroll
+          for (int t = 0; t < TU; ++t)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) u[t][j] = bounded(u[t][j]);
+        }
+#pragma unroll
+        for (int t = 0; t < TU; ++t)
+#pragma unroll
+          for (int j = 0; j < C::FN; ++j)
+            d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, low[t]),
+                                                           __builtin_bit_cast(bf16x8, u[t][j]), d[j], 0, 0, 0);
       }
 #pragma unroll
       for (int j = 0; j < C::FN; ++j)

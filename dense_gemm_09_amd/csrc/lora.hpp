@@ -91,11 +91,36 @@ __device__ __forceinline__ i32x4 load8_fix(i32x4 v, int k, int K) {
 
 __device__ __forceinline__ i32x4 load8(const uint16_t* row, int k, int K) { return load8_fix(load8_raw(row, k, K), k, K); }
 
-// high and low of h (above). Beyond BF16's range low is left out: the difference would be NaN.
+// high and low of h (above). An h that BF16 would round to an infinity has its bits cut
+// off instead; infinities and NaN are high's alone.
 __device__ __forceinline__ void split_h(float h, uint32_t& high, uint32_t& low) {
+  const uint32_t bits = __float_as_uint(h);
+  const bool finite = (bits & 0x7f800000u) != 0x7f800000u;
   high = f32_to_bf16_bits(h);
+  if (finite && (high & 0x7fffu) == 0x7f80u) high = bits >> 16;
   const float rest = h - bf16_bits_to_f32(static_cast<uint16_t>(high));
-  low = (high & 0x7f80u) == 0x7f80u ? 0u : f32_to_bf16_bits(rest);
+  low = finite ? f32_to_bf16_bits(rest) : 0u;
+}
+
+// An infinite second factor times h is an infinity with the sign of both: high gives
+// it, and low, which may be zero or of the other sign, must not turn it into NaN. Low's
+// product therefore takes the factors without their infinities (and NaN, which
+// high's product has had as well). unbounded: nonzero if the fragment has any; the
+// exponents' carries tell (three instructions for two elements).
+__device__ __forceinline__ uint32_t unbounded(const i32x4& v) {
+  uint32_t c = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) c |= (static_cast<uint32_t>(v[q]) & 0x7f807f80u) + 0x00800080u;
+  return c & 0x80008000u;
+}
+
+__device__ __forceinline__ i32x4 bounded(i32x4 v) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t c = ((static_cast<uint32_t>(v[q]) & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+    v[q] = static_cast<int>(static_cast<uint32_t>(v[q]) & ~(c | (c - (c >> 15))));
+  }
+  return v;
 }
 
 struct LoraDownArgs {
