@@ -126,11 +126,17 @@ __device__ __forceinline__ WaveAdapter wave_adapter(const LoraArgs& p, int wave,
   return a;
 }
 
+// h's parts that a kernel with this output multiplies (lora.hpp).
+template <int OUT>
+constexpr int kParts = OUT == OUT_F32 ? 3 : 2;
+
 // The lane's part of h's fragments of ranks r .. r + 31 (r + 8 (lane / 16) .. + 7 of row
 // lane % 16), the shares of K added up in their order. Rows without an adapter hold anything.
-__device__ __forceinline__ void h_fragments(const LoraArgs& p, int r, int lane, i32x4& high, i32x4& low) {
+template <int PARTS>
+__device__ __forceinline__ void h_fragments(const LoraArgs& p, int r, int lane, i32x4 (&part)[PARTS]) {
   const int at = r + 8 * (lane >> 4);
-  high = low = i32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) part[i] = i32x4{0, 0, 0, 0};
   if (at >= p.pad) return;
   const float* h = p.partial + static_cast<int64_t>(min(lane & 15, p.M - 1)) * p.pad + at;
   const int64_t next = static_cast<int64_t>(p.M) * p.pad;
@@ -141,20 +147,24 @@ __device__ __forceinline__ void h_fragments(const LoraArgs& p, int r, int lane, 
     for (int q = 0; q < 2; ++q) v[q] += *reinterpret_cast<const f32x4*>(h + s * next + 4 * q);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    uint32_t h0, l0, h1, l1;
-    split_h(v[q >> 1][2 * (q & 1)], h0, l0);
-    split_h(v[q >> 1][2 * (q & 1) + 1], h1, l1);
-    high[q] = static_cast<int>(h0 | h1 << 16);
-    low[q] = static_cast<int>(l0 | l1 << 16);
+    uint32_t even[PARTS], odd[PARTS];
+    split_h(v[q >> 1][2 * (q & 1)], even);
+    split_h(v[q >> 1][2 * (q & 1) + 1], odd);
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) part[i][q] = static_cast<int>(even[i] | odd[i] << 16);
   }
 }
 
-__device__ __forceinline__ f32x4 adapter_mfma(const i32x4& high, const i32x4& low, i32x4 up, f32x4 d) {
-  d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, high), __builtin_bit_cast(bf16x8_t, up), d,
-                                              0, 0, 0);
-  if (__any(unbounded(up) != 0)) up = bounded(up);
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, low), __builtin_bit_cast(bf16x8_t, up),
-                                                 d, 0, 0, 0);
+// d + h up, the highest part of h first.
+template <int PARTS, class Part>
+__device__ __forceinline__ f32x4 adapter_mfma(Part part, i32x4 up, f32x4 d) {
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) {
+    d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, part(i)), __builtin_bit_cast(bf16x8_t, up),
+                                                d, 0, 0, 0);
+    if (i == 0 && __any(unbounded(up) != 0)) up = bounded(up);
+  }
+  return d;
 }
 
 // d of the adapter's rows to delta[row][column].
@@ -253,9 +263,9 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_kernel(SkinnyArgs<LORA> p
         f32x4 d = {0.f, 0.f, 0.f, 0.f};
         for (int r = 0; r < p.pad; r += 32) {
           const i32x4 columns = load8(up, r + 8 * (lane >> 4), p.rank);
-          i32x4 high, low;
-          h_fragments(p, r, lane, high, low);
-          d = adapter_mfma(high, low, columns, d);
+          i32x4 part[kParts<OUT>];
+          h_fragments(p, r, lane, part);
+          d = adapter_mfma<kParts<OUT>>([&](int i) { return part[i]; }, columns, d);
         }
         store_delta(a, d, delta, lane);
       }
@@ -348,8 +358,9 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_stream_kernel(SkinnyArgs<
 
   // A: rows 0..15 (rows past M are zero lanes, never stored). With adapters, whose
   // columns need registers too, three quarters wait in LDS (in registers the kernel
-  // spilled: 16 rows, N = 18432, K = 4096: 64 us).
-  constexpr int IN_LDS = LORA ? 3 * KSM / 4 : 0;
+  // spilled: 16 rows, N = 18432, K = 4096: 64 us), and one more where h has three parts
+  // (two registers spilled: 46.0 us, so 43.8).
+  constexpr int IN_LDS = LORA ? 3 * KSM / 4 + (kParts<OUT> == 3 ? 1 : 0) : 0;
   __shared__ __attribute__((aligned(16))) Frag a_parts[LORA ? KW : 1][LORA ? IN_LDS : 1][LORA ? 64 : 1];
   Frag av[KSM];
   {
@@ -404,15 +415,21 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_stream_kernel(SkinnyArgs<
     for (int ks = 0; ks < KSM; ++ks) bv[ks] = ld(brow, kb + ks * S::KSTEP, in && ks < per);
   };
 
-  // Adapters of up to 32 ranks: h's two fragments wait in LDS.
+  // Adapters of up to 32 ranks: h's fragments wait in LDS.
   __shared__ float delta[LORA ? 2 : 1][16][16];
-  __shared__ __attribute__((aligned(16))) i32x4 h_parts[2][LORA ? 64 : 1];
+  constexpr int PARTS = kParts<OUT>;
+  __shared__ __attribute__((aligned(16))) i32x4 h_parts[LORA ? PARTS : 1][LORA ? 64 : 1];
   WaveAdapter adapter{-1, 0u, 0u};
   if constexpr (LORA) {
     static_assert(KW >= 16 && TY == TY_BF16, "a wave for every adapter");
     if (p.adapters > 0) {
       adapter = wave_adapter(p, wave, lane);
-      if (wave == 0) h_fragments(p, 0, lane, h_parts[0][lane], h_parts[1][lane]);
+      if (wave == 0) {
+        i32x4 part[PARTS];
+        h_fragments(p, 0, lane, part);
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) h_parts[i][lane] = part[i];
+      }
     }
     __syncthreads();
   }
@@ -457,8 +474,9 @@ __global__ void __launch_bounds__(KW * 64) gemm_skinny_stream_kernel(SkinnyArgs<
       }
       if constexpr (LORA) {
         if (adapter.g >= 0)
-          store_delta(adapter, adapter_mfma(h_parts[0][lane], h_parts[1][lane], load8_fix(up, 8 * (lane >> 4), p.rank),
-                                            f32x4{0.f, 0.f, 0.f, 0.f}), delta[i & 1], lane);
+          store_delta(adapter, adapter_mfma<PARTS>([&](int q) { return h_parts[q][lane]; },
+                                                   load8_fix(up, 8 * (lane >> 4), p.rank), f32x4{0.f, 0.f, 0.f, 0.f}),
+                      delta[i & 1], lane);
       }
       red[i & 1][wave][lane] = acc;
       __syncthreads();

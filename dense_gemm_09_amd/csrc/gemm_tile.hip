@@ -677,7 +677,8 @@ __device__ __forceinline__ void run_epilogue(const GemmArgs& p,
 // them requested together: it is their latency that this costs. Where K is split,
 // an adapter goes to the partial sum of its number (not of its turn in the batch:
 // a row's bits do not depend on its neighbours).
-template <class C>
+// PARTS: of h (lora.hpp).
+template <class C, int PARTS>
 __device__ __forceinline__ void add_adapters(const LoraArgs& p, f32x16 (&acc)[C::FM][C::FN], int row0,
                                              int col0, int lane, int split) {
   constexpr int TU = 2;  // 16 ranks each
@@ -692,7 +693,7 @@ __device__ __forceinline__ void add_adapters(const LoraArgs& p, f32x16 (&acc)[C:
     id = id < p.adapters ? id : -1;
     unsigned left = static_cast<unsigned>(__ballot(id >= 0));  // lanes 32.. repeat these rows
     if (left == 0) continue;
-    const uint16_t* h = p.h + static_cast<int64_t>(min(m, p.M - 1)) * (2 * p.pad) + 8 * half;
+    const uint16_t* h = p.h + static_cast<int64_t>(min(m, p.M - 1)) * (PARTS * p.pad) + 8 * half;
     do {
       const int g = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
       const unsigned rows = static_cast<unsigned>(__ballot(id == g));
@@ -706,14 +707,14 @@ __device__ __forceinline__ void add_adapters(const LoraArgs& p, f32x16 (&acc)[C:
 #pragma unroll
         for (int e = 0; e < 16; ++e) d[j][e] = 0.f;
       for (int t0 = 0; t0 < p.pad; t0 += 16 * TU) {
-        i32x4 high[TU], low[TU], u[TU][C::FN];
+        i32x4 part[PARTS][TU], u[TU][C::FN];
 #pragma unroll
         for (int t = 0; t < TU; ++t) {
           const int r = t0 + 16 * t;
-          high[t] = low[t] = i32x4{0, 0, 0, 0};
-          if (r < p.pad) {
-            high[t] = *reinterpret_cast<const i32x4*>(h + r);
-            low[t] = *reinterpret_cast<const i32x4*>(h + p.pad + r);
+#pragma unroll
+          for (int q = 0; q < PARTS; ++q) {
+            part[q][t] = i32x4{0, 0, 0, 0};
+            if (r < p.pad) part[q][t] = *reinterpret_cast<const i32x4*>(h + q * p.pad + r);
           }
 #pragma unroll
           for (int j = 0; j < C::FN; ++j) u[t][j] = load8(up[j] + at, r + 8 * half, p.rank);
@@ -724,7 +725,7 @@ __device__ __forceinline__ void add_adapters(const LoraArgs& p, f32x16 (&acc)[C:
 #pragma unroll
           for (int j = 0; j < C::FN; ++j) {
             infinite |= unbounded(u[t][j]);
-            d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, high[t]),
+            d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, part[0][t]),
                                                            __builtin_bit_cast(bf16x8, u[t][j]), d[j], 0, 0, 0);
           }
         if (__any(infinite != 0)) {
@@ -734,11 +735,13 @@ __device__ __forceinline__ void add_adapters(const LoraArgs& p, f32x16 (&acc)[C:
             for (int j = 0; j < C::FN; ++j) u[t][j] = bounded(u[t][j]);
         }
 #pragma unroll
-        for (int t = 0; t < TU; ++t)
+        for (int q = 1; q < PARTS; ++q)
 #pragma unroll
-          for (int j = 0; j < C::FN; ++j)
-            d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, low[t]),
-                                                           __builtin_bit_cast(bf16x8, u[t][j]), d[j], 0, 0, 0);
+          for (int t = 0; t < TU; ++t)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+              d[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, part[q][t]),
+                                                             __builtin_bit_cast(bf16x8, u[t][j]), d[j], 0, 0, 0);
       }
 #pragma unroll
       for (int j = 0; j < C::FN; ++j)
@@ -1342,7 +1345,7 @@ gemm_tile_kernel(ArgsOf<MODE> p) {
   const int row0 = m0 + wm0, col0 = n0 + wn0;
   if constexpr (MODE == MODE_LORA) {
     // (Without adapters there are no arrays of them to read.)
-    if (p.adapters > 0) add_adapters<C>(p, acc, row0, col0, lane, split);
+    if (p.adapters > 0) add_adapters<C, OUT == OUT_F32 ? 3 : 2>(p, acc, row0, col0, lane, split);
   }
   run_epilogue<C, OUT, SPLIT>(p, acc, elds, row0, col0, lane, split);
 }
@@ -1611,13 +1614,21 @@ hipError_t G355_WGRAD_LAUNCHER(G355_PART)(const GroupedPlan& plan, const LaunchS
 
 #elif defined(G355_LORA)
 
-template <class C>
-static hipError_t launch_lora_cfg(const Plan& plan, const LoraArgs& a, hipStream_t stream) {
-  constexpr int OUT = PART == PART_BF16 ? OUT_BF16 : OUT_F32;
+template <class C, int OUT>
+static hipError_t launch_lora_out(const Plan& plan, const LoraArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((gemm_tile_kernel<C, LOAD_DIRECT, LOAD_DIRECT, OUT, PART == PART_SPLIT,
                                        G355_RAGGED != 0, MODE_LORA>),
                      dim3(static_cast<unsigned>(plan.grid)), dim3(C::NT), 0, stream, a);
   return hipGetLastError();
+}
+
+// Partial sums are FP32 whatever the output; its type says how many parts of h they take.
+template <class C>
+static hipError_t launch_lora_cfg(const Plan& plan, const LoraArgs& a, hipStream_t stream) {
+  if constexpr (PART == PART_SPLIT) {
+    if (a.parts == 2) return launch_lora_out<C, OUT_BF16>(plan, a, stream);
+  }
+  return launch_lora_out<C, PART == PART_BF16 ? OUT_BF16 : OUT_F32>(plan, a, stream);
 }
 
 hipError_t G355_LORA_LAUNCHER(G355_RAGGED, G355_PART)(const Plan& plan, const LoraArgs& a, hipStream_t stream) {

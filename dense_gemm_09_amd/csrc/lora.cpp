@@ -35,7 +35,7 @@ constexpr int64_t kFewRows = 16;
 
 // The workspace: h, its partial sums, the product's partial sums of a split K.
 size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
-size_t h_bytes(int64_t M, int64_t R) { return rounded(static_cast<size_t>(M) * 4 * padded_rank(R)); }
+size_t h_bytes(int64_t M, int64_t R) { return rounded(static_cast<size_t>(M) * 2 * kMostParts * padded_rank(R)); }
 size_t partial_bytes(int64_t M, int64_t K, int64_t R) {
   const int shares = lora_shares(M, K, R).shares;
   return shares == 1 && M > kFewRows ? 0 : rounded(static_cast<size_t>(shares) * M * padded_rank(R) * sizeof(float));
@@ -138,6 +138,7 @@ gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R
   a.adapters = adapters ? static_cast<int>(G) : 0;
   a.rank = static_cast<int>(R);
   a.pad = static_cast<int>(padded_rank(R));
+  a.parts = parts_of_h(c_dtype == GEMM_OUT_F32);
   (void)hipGetLastError();  // an earlier call's pending error is not this call's
   if (adapters) {
     LoraDownArgs d{};
@@ -157,6 +158,7 @@ gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R
     d.adapters = a.adapters;
     d.rank = a.rank;
     d.pad = a.pad;
+    d.parts = a.parts;
     if (launch_lora_down(d, s) != hipSuccess) return GEMM_ERR_HIP;
   }
   LaunchSpec spec{};

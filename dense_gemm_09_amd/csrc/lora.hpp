@@ -16,11 +16,15 @@ inline int64_t padded_rank(int64_t R) { return (R + 15) / 16 * 16; }
 
 // The first factors' product h[m] = scale[a] * (A[m] down_a) of row m with adapter a.
 // It is summed in FP32, over shares of K where that brings more workgroups, and
-// multiplied with the second factors as two BF16 values, high = RNE(h) and
-// low = RNE(h - high): for tiles, which read it often, a row is stored as pad high parts,
-// then pad low ones; the kernels for few rows add up the shares themselves. Off by at most 2^-16 of h, where one BF16 value would be
-// off by 2^-8: as much as the output's own rounding, before it. Columns from the
-// rank on are zeros; rows without an adapter are not written.
+// multiplied with the second factors as BF16 values whose sum it is (split_h): two for
+// BF16 output, off by at most 2^-16 of h, where one value would be off by 2^-8, as much
+// as the output's own rounding, before it; three for FP32 output, which hold all of its
+// 24 bits. For tiles, which read it often, a row is stored as pad values of each part,
+// the highest first; the kernels for few rows add up the shares themselves. Columns from
+// the rank on are zeros; rows without an adapter are not written.
+constexpr int kMostParts = 3;
+inline int parts_of_h(bool f32_out) { return f32_out ? 3 : 2; }
+
 struct LoraShares {
   int shares;
   int len;  // K elements of a share, a multiple of 64
@@ -39,13 +43,14 @@ inline LoraShares lora_shares(int64_t M, int64_t K, int64_t R) {
 
 struct LoraArgs : GemmArgs {
   const int32_t* adapter;  // INT32[M]
-  const uint16_t* h;       // [M][2 * pad], tile kernels
+  const uint16_t* h;       // [M][parts * pad], tile kernels
   const float* partial;    // [shares][M][pad], kernels for few rows
   int shares;
   const uint16_t* up;      // adapter g's N rows of rank elements at g * stride_up
   int64_t ld_up, stride_up;
   int adapters;            // G
   int rank, pad;
+  int parts;               // of h
 };
 
 typedef int i32x4_any __attribute__((ext_vector_type(4), aligned(2)));
@@ -91,22 +96,31 @@ __device__ __forceinline__ i32x4 load8_fix(i32x4 v, int k, int K) {
 
 __device__ __forceinline__ i32x4 load8(const uint16_t* row, int k, int K) { return load8_fix(load8_raw(row, k, K), k, K); }
 
-// high and low of h (above). An h that BF16 would round to an infinity has its bits cut
-// off instead; infinities and NaN are high's alone.
-__device__ __forceinline__ void split_h(float h, uint32_t& high, uint32_t& low) {
+// The parts of h (above). Of two, each is rounded to nearest, except that an h which
+// BF16 would round to an infinity has its bits cut off; of three, each has its bits cut
+// off, so that the last is exact. Infinities and NaN are the highest part's alone.
+template <int PARTS>
+__device__ __forceinline__ void split_h(float h, uint32_t (&part)[PARTS]) {
   const uint32_t bits = __float_as_uint(h);
   const bool finite = (bits & 0x7f800000u) != 0x7f800000u;
-  high = f32_to_bf16_bits(h);
-  if (finite && (high & 0x7fffu) == 0x7f80u) high = bits >> 16;
-  const float rest = h - bf16_bits_to_f32(static_cast<uint16_t>(high));
-  low = finite ? f32_to_bf16_bits(rest) : 0u;
+  const uint32_t nearest = f32_to_bf16_bits(h);
+  const bool cut = PARTS == 3 || (nearest & 0x7fffu) == 0x7f80u;
+  part[0] = finite && cut ? bits >> 16 : nearest;
+  float rest = h - bf16_bits_to_f32(static_cast<uint16_t>(part[0]));
+  if constexpr (PARTS == 2) {
+    part[1] = finite ? f32_to_bf16_bits(rest) : 0u;
+  } else {
+    part[1] = finite ? __float_as_uint(rest) >> 16 : 0u;
+    rest -= bf16_bits_to_f32(static_cast<uint16_t>(part[1]));
+    part[2] = finite ? __float_as_uint(rest) >> 16 : 0u;
+  }
 }
 
-// An infinite second factor times h is an infinity with the sign of both: high gives
-// it, and low, which may be zero or of the other sign, must not turn it into NaN. Low's
-// product therefore takes the factors without their infinities (and NaN, which
-// high's product has had as well). unbounded: nonzero if the fragment has any; the
-// exponents' carries tell (three instructions for two elements).
+// An infinite second factor times h is an infinity with the sign of both: the highest
+// part gives it, and the others, which may be zero or of the other sign, must not turn
+// it into NaN. Their products therefore take the factors without their infinities (and
+// NaN, which the highest part's product has had as well). unbounded: nonzero if the
+// fragment has any; the exponents' carries tell (three instructions for two elements).
 __device__ __forceinline__ uint32_t unbounded(const i32x4& v) {
   uint32_t c = 0;
 #pragma unroll
@@ -130,9 +144,9 @@ struct LoraDownArgs {
   const uint16_t* down;
   int64_t ld_down, stride_down;
   const float* scale;  // or nullptr: ones
-  uint16_t* h;         // [M][2 * pad], or nullptr: partial sums are all that is wanted
+  uint16_t* h;         // [M][parts * pad], or nullptr: partial sums are all that is wanted
   float* partial;      // [shares][M][pad] (not used for one share and an h)
-  int M, K, adapters, rank, pad;
+  int M, K, adapters, rank, pad, parts;
   int shares, share_len;
   int split;           // workgroups that a tile's adapters are dealt to (set by the launch)
 };

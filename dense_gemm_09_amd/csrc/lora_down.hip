@@ -25,13 +25,24 @@ constexpr int kWaves = 8;
 constexpr int kTurn = 64;  // K elements of a wave's turn
 constexpr int kMaxTiles = 1 << 20;
 
-// high and low of one element (lora.hpp).
+// The parts of one element (lora.hpp).
 __device__ __forceinline__ void store_h(const LoraDownArgs& p, int m, int r, float h) {
-  uint16_t* row = p.h + static_cast<int64_t>(m) * 2 * p.pad;
-  uint32_t high, low;
-  split_h(h, high, low);
-  row[r] = static_cast<uint16_t>(high);
-  row[p.pad + r] = static_cast<uint16_t>(low);
+  uint16_t* at = p.h + static_cast<int64_t>(m) * p.parts * p.pad + r;
+  const auto store = [&](auto& part) {
+    for (const uint32_t v : part) {
+      *at = static_cast<uint16_t>(v);
+      at += p.pad;
+    }
+  };
+  if (p.parts == 3) {
+    uint32_t part[3];
+    split_h(h, part);
+    store(part);
+  } else {
+    uint32_t part[2];
+    split_h(h, part);
+    store(part);
+  }
 }
 
 }  // namespace

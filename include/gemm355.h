@@ -512,8 +512,9 @@ gemm_status gemm_combine_rows_grad(int64_t T, int64_t top_k, int64_t R, int64_t 
  * ld_down >= K. up: BF16, its N rows of R at stride_up * g, ld_up >= R.
  * (An adapter of lower rank has rows of zeros in down.) scale: FP32[G], or
  * NULL for ones. R at most 128; G == 0 or R == 0 is the plain projection.
- * Sums are FP32. scale * (A down) passes to the second product as two BF16
- * values that together keep 16 bits of it. An adapter's infinities and NaN
+ * Sums are FP32. scale * (A down) passes to the second product as BF16 values whose sum it
+ * is: two for BF16 output, which keep 16 bits of it, three for FP32 output, which keep all
+ * 24. An adapter's infinities and NaN
  * stay in its own rows. C, bias, act, beta and alpha as in gemm_bf16.
  * workspace: gemm_lora_workspace_size(M, N, K, R) bytes, 16-byte aligned.
  * Errors as for gemm_bf16; GEMM_ERR_BAD_LD also for a negative stride_down or
