@@ -182,8 +182,16 @@ __device__ __forceinline__ V larger(V a, V b) { return a > b ? a : b; }
 template <class V>
 __device__ __forceinline__ V smaller(V a, V b) { return a > b ? b : a; }
 
-// The scores of the groups, group g's in lane g: the sum of its one or two best
-// keys. In the usual case a group is 1, 2, 4, 8 or 16 lanes whole, which find its two
+template <class K, class Key>
+__device__ __forceinline__ typename K::Score group_total(const RouteArgs& p, Key best, Key second) {
+  using Score = typename K::Score;
+  if (p.group_best == 1) return K::score(best);
+  const Score half = Score(0.5) * K::score(best);
+  return second != K::none() ? half + Score(0.5) * K::score(second) : half;
+}
+
+// The scores of the groups, group g's in lane g: its best key, or half the sum of its two
+// best (the sum itself may be beyond FP32 where biases are large). In the usual case a group is 1, 2, 4, 8 or 16 lanes whole, which find its two
 // best in a butterfly, all groups at once; otherwise it is one group after another.
 template <int EPL, class Key>
 __device__ __forceinline__ typename KeyOf<Key>::Score group_scores(const RouteArgs& p, const Key (&key)[EPL], int lane) {
@@ -207,8 +215,7 @@ __device__ __forceinline__ typename KeyOf<Key>::Score group_scores(const RouteAr
     if (lanes > 2) join(across<2>(a), across<2>(b));
     if (lanes > 4) join(across<4>(a), across<4>(b));
     if (lanes > 8) join(across<8>(a), across<8>(b));
-    Score total = K::score(a);
-    if (p.group_best == 2 && b != none) total += K::score(b);
+    const Score total = group_total<K>(p, a, b);
     const Score there = __shfl(total, (lane * lanes) & 63);
     return lane < p.groups ? there : mine;
   }
@@ -222,12 +229,12 @@ __device__ __forceinline__ typename KeyOf<Key>::Score group_scores(const RouteAr
       a = larger(a, k);
     }
     const Key best = wave_max(a);
-    Score total = K::score(best);
+    Key second = none;
     if (p.group_best == 2 && best != none) {
       const int owner = __builtin_ctzll(__ballot(a == best));
-      const Key second = wave_max(lane == owner ? b : a);
-      if (second != none) total += K::score(second);
+      second = wave_max(lane == owner ? b : a);
     }
+    const Score total = group_total<K>(p, best, second);
     if (lane == g) mine = total;
   }
   return mine;
@@ -256,7 +263,7 @@ __device__ __forceinline__ bool keep_groups(const RouteArgs& p, Key (&key)[EPL],
   const float last = -wave_top(kept ? -static_cast<float>(mine) : -__builtin_inff());
   const float next = wave_top(kept ? -__builtin_inff() : static_cast<float>(mine));
   // (Groups without an expert left are -inf on both sides: inf - inf is NaN, no doubt.)
-  return last - next <= 4.f * slack;
+  return last - next <= 2.f * slack;
 }
 
 // Rounds: slot j's expert goes to lane j's id (-1: none left). With a slack, one round
