@@ -244,6 +244,22 @@ def _need_f32(t, n: int, what: str):
     _need(t, 4 * n, what)
 
 
+_kinds = {}
+
+
+def _need_kind(t, kind: int, n: int, what: str):
+    """n elements of an OUT_ kind: another type has the bytes, but is read as other numbers. A tensor of bytes is
+    taken as it is, and an unknown kind is the library's to refuse."""
+    if t is None or isinstance(t, int) or n <= 0:
+        return
+    if t.dtype is not _kinds.get(kind):
+        if not _kinds:
+            _kinds.update({OUT_F32: _dtype("float32"), OUT_BF16: _dtype("bfloat16")})
+        if t.dtype not in (_kinds.get(kind, t.dtype), _dtype("uint8")):
+            raise ValueError(f"{what} must be {'FP32' if kind == OUT_F32 else 'BF16'}, not {t.dtype}")
+    _need(t, n << (2 if kind == OUT_F32 else 1), what)
+
+
 def _extent(rows: int, cols: int, ld: int) -> int:
     """Elements spanned by a rows x cols block stored with leading dimension ld."""
     return 0 if rows == 0 or cols == 0 else (rows - 1) * ld + cols
@@ -520,7 +536,7 @@ def route(T, E, top_k, logits, ldl, l_dtype, score, bias, groups, top_groups, gr
     """
     L = lib()
     if T > 0 and E > 0 and top_k > 0:
-        _need(logits, _size(l_dtype) * _extent(T, E, ldl), "logits")
+        _need_kind(logits, l_dtype, _extent(T, E, ldl), "logits")
         _need_f32(bias, E, "bias")
         _need_int32(expert, T * top_k, "expert")
         _need_f32(weight, T * top_k, "weight")
@@ -537,10 +553,10 @@ def route_grad(T, E, top_k, logits, ldl, l_dtype, score, renormalise, scale, exp
     """dlogits (the logits' type, all E columns): the gradient of route's weights, the choice held fixed."""
     L = lib()
     if T > 0 and E > 0 and top_k > 0:
-        _need(logits, _size(l_dtype) * _extent(T, E, ldl), "logits")
+        _need_kind(logits, l_dtype, _extent(T, E, ldl), "logits")
         _need_int32(expert, T * top_k, "expert")
         _need_f32(dweight, T * top_k, "dweight")
-        _need(dlogits, _size(l_dtype) * _extent(T, E, ldd), "dlogits")
+        _need_kind(dlogits, l_dtype, _extent(T, E, ldd), "dlogits")
         if _several_devices():
             _one_device(stream, logits=logits, expert=expert, dweight=dweight, dlogits=dlogits)
     st = L.gemm_route_grad(T, E, top_k, _ptr(logits), ldl, l_dtype, score, 1 if renormalise else 0, scale,
@@ -575,6 +591,9 @@ def dispatch_rows(T, top_k, R, N, X, ldx, elem_bytes, position, Y, ldy, stream=N
     """Y[position[t, j]] = X[t]: rows of N elements of 1, 2 or 4 bytes; positions outside [0, R) are passed over."""
     L = lib()
     if T > 0 and top_k > 0 and R > 0 and N > 0:
+        for t, what in ((X, "X"), (Y, "Y")):
+            if t is not None and not isinstance(t, int) and t.element_size() not in (1, elem_bytes):
+                raise ValueError(f"{what}'s elements have {t.element_size()} bytes, not {elem_bytes}")
         _need(X, elem_bytes * _extent(T, N, ldx), "X")
         _need_int32(position, T * top_k, "position")
         _need(Y, elem_bytes * _extent(R, N, ldy), "Y")
@@ -590,10 +609,10 @@ def combine_rows(T, top_k, R, N, Y, ldy, y_dtype, position, weight, beta, C, ldc
     """C[t] = sum_j weight[t, j] * Y[position[t, j]] + beta * C[t] (weight None: ones), summed in FP32."""
     L = lib()
     if T > 0 and top_k > 0 and N > 0:
-        _need(Y, _size(y_dtype) * _extent(R, N, ldy), "Y")
+        _need_kind(Y, y_dtype, _extent(R, N, ldy), "Y")
         _need_int32(position, T * top_k, "position")
         _need_f32(weight, T * top_k, "weight")
-        _need(C, _size(c_dtype) * _extent(T, N, ldc), "C")
+        _need_kind(C, c_dtype, _extent(T, N, ldc), "C")
         if _several_devices():
             _one_device(stream, Y=Y, position=position, weight=weight, C=C)
     st = L.gemm_combine_rows(T, top_k, R, N, _ptr(Y), ldy, y_dtype, _ptr(position), _ptr(weight), beta, _ptr(C), ldc,
@@ -608,10 +627,10 @@ def combine_rows_grad(T, top_k, R, N, D, ldd, d_dtype, Y, ldy, y_dtype, position
     L = lib()
     if T > 0 and top_k > 0:
         if N > 0 and R > 0:
-            _need(D, _size(d_dtype) * _extent(T, N, ldd), "D")
+            _need_kind(D, d_dtype, _extent(T, N, ldd), "D")
             if dweight is not None:
-                _need(Y, _size(y_dtype) * _extent(R, N, ldy), "Y")
-            _need(dY, _size(y_dtype) * _extent(R, N, lddy), "dY")
+                _need_kind(Y, y_dtype, _extent(R, N, ldy), "Y")
+            _need_kind(dY, y_dtype, _extent(R, N, lddy), "dY")
         _need_int32(position, T * top_k, "position")
         _need_f32(weight, T * top_k, "weight")
         _need_f32(dweight, T * top_k, "dweight")
@@ -637,12 +656,16 @@ def gemm_lora_bf16(M, N, K, G, R, alpha, A, lda, B, ldb, adapter, down, ld_down,
     rows of K, up: G times N rows of R; scale: FP32[G] or None. With workspace=None one is allocated here.
     """
     L = lib()
-    _check_operands(M, N, K, A, lda, ROW, B, ldb, COL, C, ldc, c_dtype, 2, bias)
-    if M > 0 and N > 0 and G > 0 and R > 0:
-        _need_int32(adapter, M, "adapter")
-        _need(down, 2 * ((G - 1) * stride_down + _extent(R, K, ld_down)) if K > 0 else 0, "down")
-        _need(up, 2 * ((G - 1) * stride_up + _extent(N, R, ld_up)), "up")
-        _need_f32(scale, G, "scale")
+    if M > 0 and N > 0:
+        _need_kind(A, OUT_BF16, _extent(M, K, lda), "A")
+        _need_kind(B, OUT_BF16, _extent(N, K, ldb), "B")
+        _need_kind(C, c_dtype, _extent(M, N, ldc), "C")
+        _need_kind(bias, OUT_BF16, N, "bias")
+        if G > 0 and R > 0:
+            _need_int32(adapter, M, "adapter")
+            _need_kind(down, OUT_BF16, (G - 1) * stride_down + _extent(R, K, ld_down) if K > 0 else 0, "down")
+            _need_kind(up, OUT_BF16, (G - 1) * stride_up + _extent(N, R, ld_up), "up")
+            _need_f32(scale, G, "scale")
     if M > 0 and N > 0 and _several_devices():
         _one_device(stream, A=A, B=B, adapter=adapter, down=down, up=up, scale=scale, C=C, bias=bias,
                     workspace=workspace)
