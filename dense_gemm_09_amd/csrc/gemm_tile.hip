@@ -1635,8 +1635,12 @@ hipError_t G355_LORA_LAUNCHER(G355_RAGGED, G355_PART)(const Plan& plan, const Lo
   if (plan.bm == 64)
     return plan.bn == 256 ? launch_lora_cfg<Thin16>(plan, a, stream) : launch_lora_cfg<Narrow16>(plan, a, stream);
   if (plan.bm == 256 && plan.bn == 256) return launch_lora_cfg<Big16>(plan, a, stream);
-  if (plan.bm == 256) return launch_lora_cfg<Mid16>(plan, a, stream);
-  if constexpr (PART != PART_SPLIT) {
+  // 256x128 tiles come with a split K only: whole, 128x128 ones take at most as many
+  // rounds, and less time in each (make_tile_plan).
+  if constexpr (PART == PART_SPLIT) {
+    if (plan.bm == 256) return launch_lora_cfg<Mid16>(plan, a, stream);
+  } else {
+    if (plan.bm == 256) return hipErrorInvalidValue;
     if (plan.grid <= kDeepGrid) return launch_lora_cfg<Deep16>(plan, a, stream);
   }
   return launch_lora_cfg<Small16>(plan, a, stream);
