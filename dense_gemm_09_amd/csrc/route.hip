@@ -147,6 +147,15 @@ __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp
 // log of the logistic function, without overflow on either side.
 __device__ __forceinline__ float log_sigmoid(float x) { return fminf(x, 0.f) - log1pf(expf(-fabsf(x))); }
 
+// exp(a - b), with what the rounding of the difference drops: up to 2^-24 of it, which
+// the exponential would turn into an error that grows with the distance (of a logit 80
+// below the largest: 64 last bits). Finite a and b, or an a of -inf.
+__device__ __forceinline__ float exp_difference(float a, float b) {
+  const float d = a - b, s = d - a;
+  const float dropped = (a - (d - s)) - (b + s);
+  return expf(d) * (d > -__FLT_MAX__ ? 1.f + dropped : 1.f);
+}
+
 }  // namespace
 
 // ------------------------------------------------------------------ choice
@@ -419,11 +428,11 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(E
       if (p.renormalise) {
         const float ls = p.sigmoid ? log_sigmoid(xj) : xj;
         const float most = wave_top(id >= 0 ? ls : ninf);
-        const float s = id >= 0 ? expf(ls - most) : 0.f;
+        const float s = id >= 0 ? exp_difference(ls, most) : 0.f;
         const float z = wave_sum(s);
         w = id >= 0 ? p.scale * (s / z) : 0.f;
       } else if (id >= 0) {
-        w = p.scale * (p.sigmoid ? expf(log_sigmoid(xj)) : expf(xj - base) / sum);
+        w = p.scale * (p.sigmoid ? expf(log_sigmoid(xj)) : exp_difference(xj, base) / sum);
       }
     }
     if (lane < p.top_k) {
