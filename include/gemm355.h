@@ -387,11 +387,13 @@ gemm_status gemm_grouped_bf16_wgrad(int64_t G, int64_t T, int64_t N, int64_t K, 
  *   expert[t, 0..top_k-1] = the experts of the top_k largest c, largest first
  *   weight[t, j] = scale * s_j, or scale * s_j / sum over the chosen s (renormalise != 0)
  *
- * Equal values go to the lowest index, of experts as of groups. The choice is
- * that of exact arithmetic: without bias (and with one best per group) it
- * compares the logits themselves, otherwise scores in 64 bits. Weights are
- * FP32; renormalised ones are formed from the scores' logarithms, so that
- * scores too small for FP32 still have shares.
+ * Equal values go to the lowest index, of experts as of groups. Without bias (and with
+ * one group or one best of each) the logits themselves are compared, which is exact.
+ * Otherwise scores formed in 64 bits are, and what those do not tell apart is equal:
+ * sigmoids of logits above 37 are all 1, softmax scores of logits 746 below the row's
+ * largest all 0, and a bias of 2^53 leaves nothing of a score. Weights are FP32;
+ * renormalised ones are formed from the scores' logarithms, so that scores too small
+ * for FP32 still have shares.
  * An expert whose logit (or bias) is -inf is not available. A token with fewer
  * than top_k available experts (in its groups) has expert -1 and weight 0 in
  * the slots that are left: a row that is all -inf, such as padding, in all of
