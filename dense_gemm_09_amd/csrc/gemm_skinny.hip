@@ -577,8 +577,12 @@ hipError_t launch_skinny(const Plan& plan, const LaunchSpec& spec, const GemmArg
 }
 
 // The product with adapters, M <= 16: the streaming kernel holds one fragment of ranks
-// (32), the other any number (16 rows, N = 18432, K = 4096 in all: 43 us, with tiles of 64
-// rows and their reduction 50; one row, N = 4096: 14 us and 20).
+// (32), the other any number. All launches together, here and on tiles of 64 rows with
+// their reduction: rank 16, N = 18432, K = 4096, an adapter to each row: one row 35.6 and
+// 38.6 us, 16 rows 41.7 and 46.6 (17 rows, on tiles: 46.9); N = 4096: 14.7 and 19.7, 17.5 and
+// 22.4 (17 rows: 22.4). Rank 64 on the other kernel, N = 4096, K = 14336: one row 31.6 and
+// 35.1, 8 rows 38.4 and 37.8, 16 rows 45.4 and 40.6; N = 14336, K = 4096: 36.3 and 33.3, 46.9
+// and 39.3, 64.8 and 53.1: tiles would be faster there.
 template <int OUT>
 static hipError_t launch_skinny_lora_out(const LoraArgs& a, hipStream_t stream) {
   constexpr int KW = 16, KSM = 8, NBUF = 2;

@@ -30,7 +30,8 @@ bool under_2g(int64_t rows, int64_t K, int64_t ld) {
 }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// Rows up to which the kernels for few rows (gemm_skinny.hip) are used.
+// Rows up to which the kernels for few rows (gemm_skinny.hip) are used; what they and
+// the tiles measure is there.
 constexpr int64_t kFewRows = 16;
 
 // The workspace: h, its partial sums, the product's partial sums of a split K.
@@ -96,8 +97,10 @@ gemm_status gemm_lora_bf16(int64_t M, int64_t N, int64_t K, int64_t G, int64_t R
 
   Plan plan = make_tile_plan(M, N, K, false);
   // Tiles of 128x128 that the dense product splits in two and that the CUs hold at
-  // once take two groups of waves along K in one workgroup instead: no partial sums
-  // (777 x 4093 x 4099, FP32: 102 -> 89 us; 1024 x 4096 x 4096: 61 -> 57).
+  // once take two groups of waves along K in one workgroup instead: no partial sums.
+  // BF16 output, split in two -> two groups: 777 x 4093 x 4099 90 -> 79 us, 1024 x 4096 x
+  // 4096 61 -> 56, 512 x 8192 x 4096 60 -> 53, 777 x 4096 x 4096 55 -> 54; the other way
+  // for 1500 x 2048 x 4096 (192 tiles) 55 -> 56 and 1100 x 3584 x 7168 86 -> 88.
   const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128);
   if (plan.bm == 128 && plan.split == 2 && tiles <= 256) {
     plan.split = 1;

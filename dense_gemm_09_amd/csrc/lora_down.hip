@@ -7,12 +7,15 @@
 // product's row depends on that row of A alone: nothing passes between requests.)
 // The waves' sums are added in LDS in the order of the waves, the shares in theirs.
 //
-// Bound by the lines that a CU's loads touch (16 rows of 64 bytes each; the same bytes
-// from one row take a third of the time), so that only rows that have the adapter
-// are read, and the reads are spread over the CUs: few rows have shares of K and
+// Bound by the latency of its loads: a wave's are all in flight at once, a request to L2
+// takes 500 to 1000 cycles, and the units that return data have some pending for 80% of
+// the CUs' cycles. That a load touches 16 rows of 64 bytes (64 cache accesses, 16 if it
+// took one row's 1024 bytes) is 13% of it: 12.0 us, 10.4 with loads of one row each, for
+// 4096 rows, K = 4096, R = 16 and an adapter to every 16 rows. So only rows that have the
+// adapter are read, and the reads are spread over the CUs: few rows have shares of K and
 // adapters in workgroups of their own (a launch of more workgroups than that costs more than they
-// bring: about 455 waves start in a microsecond). Measured: 4096 rows, K = 4096,
-// R = 16, 18 us; 64 rows of 24 adapters, K = 14336, R = 64, 17 us (44 MB of adapters:
+// bring: about 455 waves start in a microsecond). Measured: the same 4096 rows of six
+// requests 16 us; 64 rows of 24 adapters, K = 14336, R = 64, 17 us (44 MB of adapters:
 // 9 us at a copy's rate); one row 4 us.
 
 #include "lora.hpp"
